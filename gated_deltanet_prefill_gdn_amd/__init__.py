@@ -55,6 +55,9 @@ EXPORTED = ("gdn_prefill_workspace_size", "gdn_prefill_state_schedule", "gdn_pre
             "gdn_prefill_fwd_events", "gdn_prefill_fwd_noalloc", "gdn_prefill_nonfinite",
             "gdn_prefill_bwd_workspace_size", "gdn_prefill_bwd",
             "gdn_decode_fwd", "gdn_recurrent_fwd", "gdn_promote_scan", "gdn_validate_inputs",
+            "gdn_conv_fwd", "gdn_conv_decode_fwd", "gdn_conv_bwd_workspace_size", "gdn_conv_bwd",
+            "gdn_ssm_workspace_size", "gdn_ssm_prefill_fwd", "gdn_ssm_decode_fwd",
+            "gdn_norm_fwd", "gdn_norm_bwd_workspace_size", "gdn_norm_bwd",
             "gdn_status_str", "gdn_version")
 
 
@@ -135,6 +138,8 @@ def load_library(path: str = LIB_PATH):
     L.gdn_status_str.argtypes = [ctypes.c_int]
     L.gdn_version.restype = ctypes.c_int32
     L.gdn_version.argtypes = []
+    from . import layer
+    layer.declare(L)
     if path == LIB_PATH:
         _lib = L
     return L
@@ -486,3 +491,19 @@ def gdn_validate_inputs(cu_seqlens, cache_indices, prob: GdnProblem, stream=None
     st = (stream or torch.cuda.current_stream(cu_seqlens.device)).cuda_stream
     return int(load_library().gdn_validate_inputs(_ptr(cu_seqlens), _ptr(cache_indices),
                                                   ctypes.byref(prob), ctypes.c_void_p(st)))
+
+
+# The layer operators (layer.py imports torch, which this module only does when it is called).
+_LAYER = ("GDN_CONV_SILU", "GDN_NORM_RMS", "GDN_NORM_GATE_FIRST", "GdnConvProblem",
+          "GdnNormProblem", "conv_problem", "norm_problem", "gdn_conv_fwd",
+          "gdn_conv_decode_fwd", "gdn_conv_bwd_workspace_size", "gdn_conv_bwd",
+          "gdn_ssm_workspace_size", "gdn_ssm_prefill_fwd", "gdn_ssm_decode_fwd", "gdn_norm_fwd",
+          "gdn_norm_bwd_workspace_size", "gdn_norm_bwd")
+
+
+def __getattr__(name):
+    if name in _LAYER:
+        from . import layer
+        globals().update({n: getattr(layer, n) for n in _LAYER})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,185 @@
+// Selective state space scan, token by token.
+//
+//   d = softplus(dt + dt_bias),  a = exp(-exp(A_log) d),  S <- a S + d x B^T,  out = S C + D x
+//
+// Row i of S (dv x dk, fp32) depends on x[i] alone, so rows are independent: a group of dk / 8
+// lanes holds one row, 8 fp32 per lane, and a workgroup covers kRowsPerBlock rows of one
+// (request, head). The state is read once, stays in registers over the request's tokens and is
+// written once. With one token per request (decode) the kernel is bound by the state's bytes.
+#include "gdn_layer.h"
+
+namespace gdn {
+namespace layer {
+namespace {
+
+constexpr int kTokenThreads = 256;
+// A workgroup covers 64 rows at dk = 64 and 128 and 32 at dk = 256: a divisor of every dv.
+template <int DK>
+constexpr int kRowsPerThread = DK == 64 ? 2 : 4;
+template <int DK>
+constexpr int kRowsPerBlock = (64 / (DK / 8)) * kRowsPerThread<DK> * (kTokenThreads / 64);
+static_assert(kRowsPerBlock<64> == 64 && kRowsPerBlock<128> == 64 && kRowsPerBlock<256> == 32,
+              "a workgroup's rows divide dv");
+
+__device__ __forceinline__ float softplusf(float x) {
+  return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
+}
+
+// x from another lane of the same 16-lane row, chosen by a DPP control code.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
+}
+
+// Sum over an aligned group of LPR lanes, left in every lane of it.
+template <int LPR>
+__device__ __forceinline__ float group_sum(float x) {
+  static_assert(LPR == 8 || LPR == 16 || LPR == 32, "8 to 32 lanes per row");
+  x += dpp<0xB1>(x);   // lane ^ 1
+  x += dpp<0x4E>(x);   // lane ^ 2
+  x += dpp<0x141>(x);  // the other quad of the half-row, mirrored
+  if constexpr (LPR >= 16) x += dpp<0x140>(x);  // the other half of the row, mirrored
+  if constexpr (LPR >= 32) x += __shfl_xor(x, 16, 64);
+  return x;
+}
+
+// This lane's eight entries of a row of DK: 4 gl .. and DK / 2 + 4 gl .., so that a wave's load
+// covers contiguous half rows.
+template <int DK>
+__device__ __forceinline__ void load8(const float* row, int gl, float (&x)[8]) {
+  const f32x4 lo = *reinterpret_cast<const f32x4*>(row + 4 * gl);
+  const f32x4 hi = *reinterpret_cast<const f32x4*>(row + DK / 2 + 4 * gl);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = lo[i];
+    x[4 + i] = hi[i];
+  }
+}
+template <int DK>
+__device__ __forceinline__ void load8(const __bf16* row, int gl, float (&x)[8]) {
+  const bf16x4 lo = *reinterpret_cast<const bf16x4*>(row + 4 * gl);
+  const bf16x4 hi = *reinterpret_cast<const bf16x4*>(row + DK / 2 + 4 * gl);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = (float)lo[i];
+    x[4 + i] = (float)hi[i];
+  }
+}
+
+// cu == nullptr: one token per request, row b.
+template <int DK, typename T>
+__global__ __launch_bounds__(kTokenThreads) void ssm_token_kernel(
+    const T* __restrict__ cm, const T* __restrict__ bm, const T* __restrict__ x,
+    const float* __restrict__ dt, const float* __restrict__ A_log,
+    const float* __restrict__ dt_bias, const float* __restrict__ D,
+    float* __restrict__ state_pool, const int64_t* __restrict__ idx,
+    const int64_t* __restrict__ cu, T* __restrict__ out, int64_t N, int64_t pool, int H, int HV,
+    int DV, int nrb) {
+  constexpr int LPR = DK / 8, RPW = 64 / LPR, NR = kRowsPerThread<DK>, RWV = RPW * NR;
+  const uint32_t pair = blockIdx.x / (uint32_t)nrb;
+  const int rb = (int)(blockIdx.x - pair * (uint32_t)nrb);
+  const uint32_t b = pair / (uint32_t)HV;
+  const int hv = (int)(pair - b * (uint32_t)HV), h = hv / (HV / H);
+  int64_t t = b, t_end = (int64_t)b + 1;
+  if (cu) {
+    t = cu[b] < 0 ? 0 : cu[b];
+    t_end = cu[b + 1] < N ? cu[b + 1] : N;
+  }
+  const int64_t slot = idx[b];
+  if (t >= t_end || slot < 0 || slot >= pool) return;
+  const int l = threadIdx.x & 63, gl = l % LPR;
+  const int r0 = rb * kRowsPerBlock<DK> + (threadIdx.x >> 6) * RWV + l / LPR;
+  float* const sp = state_pool + ((slot * HV + hv) * (int64_t)DV + r0) * DK + 4 * gl;
+  f32x4 s[NR][2];
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    s[j][0] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(sp + j * RPW * DK));
+    s[j][1] =
+        __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(sp + j * RPW * DK + DK / 2));
+  }
+  const float decay = expf(A_log[hv]), dtb = dt_bias[hv], dd = D ? D[hv] : 0.f;
+  for (; t < t_end; ++t) {
+    const int64_t th = t * HV + hv;
+    float bb[8], cc[8], xr[NR];
+    load8<DK>(bm + (t * H + h) * DK, gl, bb);
+    load8<DK>(cm + (t * H + h) * DK, gl, cc);
+#pragma unroll
+    for (int j = 0; j < NR; ++j) xr[j] = (float)x[th * DV + r0 + j * RPW];
+    const float step = softplusf(dt[th] + dtb), a = expf(-decay * step);
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+      const float u = step * xr[j];
+      float o = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float se = __builtin_fmaf(a, s[j][e / 4][e % 4], u * bb[e]);
+        s[j][e / 4][e % 4] = se;
+        o = __builtin_fmaf(se, cc[e], o);
+      }
+      o = group_sum<LPR>(o);
+      if (gl == 0) out[th * DV + r0 + j * RPW] = (T)__builtin_fmaf(dd, xr[j], o);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    __builtin_nontemporal_store(s[j][0], reinterpret_cast<f32x4*>(sp + j * RPW * DK));
+    __builtin_nontemporal_store(s[j][1], reinterpret_cast<f32x4*>(sp + j * RPW * DK + DK / 2));
+  }
+}
+
+int rows_per_block(int dk) { return dk == 256 ? kRowsPerBlock<256> : kRowsPerBlock<128>; }
+
+int64_t token_blocks(const SsmShape& s) { return s.B * s.HV * (s.dv / rows_per_block(s.dk)); }
+
+template <int DK, typename T>
+hipError_t launch_token(const SsmShape& s, const void* C, const void* B, const void* x,
+                        const float* dt, const float* A_log, const float* dt_bias, const float* D,
+                        float* state, const int64_t* idx, const int64_t* cu, void* out,
+                        hipStream_t st) {
+  hipLaunchKernelGGL((ssm_token_kernel<DK, T>), dim3((unsigned)token_blocks(s)),
+                     dim3(kTokenThreads), 0, st, (const T*)C, (const T*)B, (const T*)x, dt, A_log,
+                     dt_bias, D, state, idx, cu, (T*)out, s.N, s.pool, s.H, s.HV, s.dv,
+                     s.dv / kRowsPerBlock<DK>);
+  return hipGetLastError();
+}
+
+hipError_t launch_token_any(const SsmShape& s, const void* C, const void* B, const void* x,
+                            const float* dt, const float* A_log, const float* dt_bias,
+                            const float* D, float* state, const int64_t* idx, const int64_t* cu,
+                            void* out, hipStream_t st) {
+#define GDN_SSM_CASE(DK)                                                                        \
+  if (s.dk == DK)                                                                               \
+    return s.bf16 ? launch_token<DK, __bf16>(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu, \
+                                             out, st)                                           \
+                  : launch_token<DK, float>(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu,  \
+                                            out, st);
+  GDN_SSM_CASE(64)
+  GDN_SSM_CASE(128)
+  GDN_SSM_CASE(256)
+#undef GDN_SSM_CASE
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+size_t ssm_workspace(const SsmShape&) { return 256; }
+
+bool ssm_grids_fit(const SsmShape& s, bool) { return grid_ok(token_blocks(s), kTokenThreads); }
+
+hipError_t launch_ssm_prefill(const SsmShape& s, const void* C, const void* B, const void* x,
+                              const float* dt, const float* A_log, const float* dt_bias,
+                              const float* D, float* state, const int64_t* idx,
+                              const int64_t* cu, void* out, char*, hipStream_t st) {
+  return launch_token_any(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu, out, st);
+}
+
+hipError_t launch_ssm_decode(const SsmShape& s, const void* C, const void* B, const void* x,
+                             const float* dt, const float* A_log, const float* dt_bias,
+                             const float* D, float* state, const int64_t* idx, void* out,
+                             hipStream_t st) {
+  return launch_token_any(s, C, B, x, dt, A_log, dt_bias, D, state, idx, nullptr, out, st);
+}
+
+}  // namespace layer
+}  // namespace gdn

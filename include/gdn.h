@@ -1,6 +1,8 @@
 /*
  * libgdn -- Gated DeltaNet chunkwise prefill forward (with the decode step that follows
- * it, and the Promote update scan of the nested variant) on MI355X (gfx950).
+ * it, and the Promote update scan of the nested variant) on MI355X (gfx950), the short
+ * convolution and the gated norm that stand around it in a layer, and the selective state
+ * space scan.
  *
  * The operation (pymllm gdn_chunkwise page, "gdn_extend_chunkwise", Module
  * Contents; the recurrence is the state-transition equation of "Simple math to
@@ -314,6 +316,144 @@ typedef struct {
 gdn_status_t gdn_promote_scan(const void* K, const void* V, const float* beta, const float* w,
                               const float* gamma, float* M, float* states,
                               const gdn_promote_problem_t* prob, void* stream);
+
+/* ---- What stands on either side of the recurrence in a layer: the short causal
+ * convolution in front of it, a gated layer or RMS norm behind it, and the selective state
+ * space scan as a recurrence of its own. Conventions shared by these calls:
+ *   - DEVICE pointers unless said otherwise; parameters (weights, biases, A_log, ...) and
+ *     gradients of parameters are fp32; nothing is allocated, every call is asynchronous on
+ *     `stream`, deterministic (no atomics), and can be captured into a HIP graph.
+ *   - cu_seqlens [B + 1] and cache_indices [B] as for gdn_prefill_fwd, except that
+ *     cu_seqlens[B] may be smaller than N: rows from cu_seqlens[B] on are padding and are
+ *     neither read nor written. A request whose cache index lies outside [0, pool) is padding
+ *     too: none of its rows and no state is written. The indices in range are distinct.
+ *   - Offsets are 64-bit; strides are in elements. Outputs may not overlap inputs.
+ *   - Errors: host checks before any launch (GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED,
+ *     GDN_ERR_WORKSPACE), GDN_ERR_HIP if a launch failed. */
+
+/* Shape of one short causal convolution (host struct). */
+typedef struct {
+  int64_t total_tokens; /* N: rows of x and of the outputs                               */
+  int64_t batch;        /* B: requests                                                   */
+  int64_t pool_size;    /* slots in state_pool (ignored when state_pool is NULL)         */
+  int64_t x_stride;     /* elements between rows of x, at least the channels             */
+  int64_t dx_stride;    /* elements between rows of dx (gdn_conv_bwd), likewise          */
+  int32_t channels[3];  /* channels of out0, out1, out2; [0] > 0, the others may be 0    */
+  int32_t width;        /* W: taps, 2 to 4                                               */
+  int32_t dtype;        /* gdn_dtype_t of x, the outputs, state_pool and dx              */
+  int32_t dout_dtype;   /* gdn_dtype_t of dout0 .. dout2 (gdn_conv_bwd)                  */
+  int32_t flags;        /* GDN_CONV_SILU or 0                                            */
+  int32_t reserved;     /* must be 0                                                     */
+} gdn_conv_problem_t;
+#define GDN_CONV_SILU 1 /* out = silu(pre) instead of pre */
+
+/* The depthwise causal convolution over each request's tokens that feeds q, k and v of
+ * gdn_prefill_fwd (or x, B and C of gdn_ssm_prefill_fwd) from one packed projection row.
+ * With CH = channels[0] + [1] + [2] and u = the request's W - 1 history rows followed by its
+ * tokens (row W - 1 + p of u is token p):
+ *   pre[p, c] = bias[c] + sum_{j < W} weight[c, j] u[p + j, c],  out = silu(pre) or pre,
+ *   state_pool[slot] <- the last W - 1 rows of u                          (in place)
+ *   x          [N, CH] rows x_stride apart, dtype (a slice of a wider row is fine)
+ *   weight     [CH, W] fp32; bias [CH] fp32 or NULL
+ *   state_pool [pool, W - 1, CH] dtype, oldest row first; NULL: zero history, none kept (then
+ *              cache_indices is not read and may be NULL)
+ *   out0 .. 2  [N, channels[i]] dense, dtype: the channels of out0 first. NULL where
+ *              channels[i] is 0.
+ * A request without tokens keeps its state. fp32 arithmetic, outputs rounded once. Vectors of
+ * 16 bytes where all pointers, strides and channel counts allow it, else element by element. */
+gdn_status_t gdn_conv_fwd(const void* x, const float* weight, const float* bias, void* state_pool,
+                          const int64_t* cache_indices, const int64_t* cu_seqlens, void* out0,
+                          void* out1, void* out2, const gdn_conv_problem_t* prob, void* stream);
+
+/* gdn_conv_fwd for one new token per request: row b of x belongs to request b, N == B
+ * (GDN_ERR_INVALID_ARG otherwise), state_pool is required. The result is that of gdn_conv_fwd
+ * with cu_seqlens = {0, 1, ..., B}, bit for bit. */
+gdn_status_t gdn_conv_decode_fwd(const void* x, const float* weight, const float* bias,
+                                 void* state_pool, const int64_t* cache_indices, void* out0,
+                                 void* out1, void* out2, const gdn_conv_problem_t* prob,
+                                 void* stream);
+
+/* Gradients of gdn_conv_fwd, for the scalar
+ *   L = sum_i <dout_i, out_i> + sum_b <dstate[b], request b's final state>.
+ *   state_pool: the pool as it was BEFORE the forward call (read only), or NULL as there
+ *   dout0 .. 2 [N, channels[i]] dense, dout_dtype (the fp32 dq, dk, dv of gdn_prefill_bwd, say)
+ *   dstate     [B, W - 1, CH] fp32, or NULL for zero
+ *   dx         [N, CH] rows dx_stride apart, dtype
+ *   dweight    [CH, W], dbias [CH] fp32 (dbias NULL if bias is NULL)
+ *   dstate0    [B, W - 1, CH] fp32: gradient of each request's history; NULL to skip
+ * dx, dweight, dbias and dstate0 are overwritten (dx on requests' rows). Padding requests
+ * add nothing and their dstate0 is zero. workspace: at least gdn_conv_bwd_workspace_size
+ * bytes, 256-byte aligned (partial sums of the parameters' gradients, added in a fixed order). */
+size_t gdn_conv_bwd_workspace_size(const gdn_conv_problem_t* prob);
+gdn_status_t gdn_conv_bwd(const void* x, const float* weight, const float* bias,
+                          const void* state_pool, const int64_t* cache_indices,
+                          const int64_t* cu_seqlens, const void* dout0, const void* dout1,
+                          const void* dout2, const float* dstate, void* dx, float* dweight,
+                          float* dbias, float* dstate0, const gdn_conv_problem_t* prob,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* The selective state space scan: the linear recurrence with a decay per head and an outer
+ * product write, without the removal term of the delta rule, on the same packing, pool and
+ * gates as gdn_prefill_fwd. For every request, head hv and group h = hv / (HV / H):
+ *   d_t = softplus(dt[t,hv] + dt_bias[hv]),  a_t = exp(-exp(A_log[hv]) d_t)
+ *   S  <- a_t S + d_t x[t,hv] B[t,h]^T,      out[t,hv] = S C[t,h] + D[hv] x[t,hv]
+ * The descriptor is gdn_problem_t with head_k the state size and head_v the head size (64, 128
+ * or 256 each), num_qk_heads the groups that share B and C, and flags 0:
+ *   C, B [N, H, dk], x, out [N, HV, dv] in qkv_dtype; dt [N, HV] fp32; A_log, dt_bias [HV] fp32;
+ *   D [HV] fp32 or NULL for zero; state_pool [pool, HV, dv, dk] fp32, updated in place.
+ * C, B, x, out and state_pool 16-byte aligned. workspace: at least gdn_ssm_workspace_size bytes,
+ * 256-byte aligned; its contents on entry do not matter. N == 0 or B == 0 is a no-op. */
+size_t gdn_ssm_workspace_size(const gdn_problem_t* prob);
+gdn_status_t gdn_ssm_prefill_fwd(const void* C, const void* B, const void* x, const float* dt,
+                                 const float* A_log, const float* dt_bias, const float* D,
+                                 float* state_pool, const int64_t* cache_indices,
+                                 const int64_t* cu_seqlens, void* out, const gdn_problem_t* prob,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* One step of the scan: row b of C, B, x, dt and out belongs to request b, N == B
+ * (GDN_ERR_INVALID_ARG otherwise). No workspace. Arithmetic in fp32. */
+gdn_status_t gdn_ssm_decode_fwd(const void* C, const void* B, const void* x, const float* dt,
+                                const float* A_log, const float* dt_bias, const float* D,
+                                float* state_pool, const int64_t* cache_indices, void* out,
+                                const gdn_problem_t* prob, void* stream);
+
+/* Shape of one norm (host struct). */
+typedef struct {
+  int64_t total_tokens; /* N                                                             */
+  int64_t x_stride;     /* elements between the tokens of x, at least heads * dim        */
+  int64_t z_stride;     /* ... of the gate z, likewise (0 when z is NULL)                */
+  int64_t dz_stride;    /* ... of dz (gdn_norm_bwd), likewise                            */
+  int32_t heads;        /* rows per token                                                */
+  int32_t dim;          /* entries of a row, 1 to 16384                                  */
+  int32_t dtype;        /* gdn_dtype_t of x, z, out, dout, dx and dz                     */
+  int32_t flags;        /* GDN_NORM_* bits                                               */
+  float eps;            /* added to the variance, not negative                           */
+  int32_t reserved;     /* must be 0                                                     */
+} gdn_norm_problem_t;
+#define GDN_NORM_RMS 1        /* divide by the root mean square: no mean is taken off         */
+#define GDN_NORM_GATE_FIRST 2 /* the gate multiplies the norm's input instead of its output   */
+
+/* Layer norm or RMS norm of every row (N * heads of them, `dim` long), with an optional gate:
+ *   u = x, or x silu(z) with GDN_NORM_GATE_FIRST;
+ *   hat = (u - mean(u)) / sqrt(mean((u - mean(u))^2) + eps)   (RMS: without mean(u))
+ *   out = hat weight + bias, times silu(z) if a gate is given and does not come first.
+ *   x, z [N, heads, dim], tokens x_stride and z_stride apart; z may be NULL
+ *   weight [dim], bias [dim] fp32, shared by the heads; bias may be NULL
+ *   out [N, heads, dim] dense
+ * fp32 statistics and arithmetic, one rounding at the end. N == 0 is a no-op. */
+gdn_status_t gdn_norm_fwd(const void* x, const float* weight, const float* bias, const void* z,
+                          void* out, const gdn_norm_problem_t* prob, void* stream);
+
+/* Gradients of gdn_norm_fwd for L = <dout, out>: dx [N, heads, dim] dense and dz (tokens
+ * dz_stride apart, NULL if z is NULL) in dtype, dweight [dim] and dbias [dim] fp32 (dbias NULL
+ * if bias is NULL), summed over all rows in a fixed order. dout [N, heads, dim] dense. All
+ * overwritten; N == 0 writes zero dweight and dbias. workspace: at least
+ * gdn_norm_bwd_workspace_size bytes, 256-byte aligned. */
+size_t gdn_norm_bwd_workspace_size(const gdn_norm_problem_t* prob);
+gdn_status_t gdn_norm_bwd(const void* x, const float* weight, const float* bias, const void* z,
+                          const void* dout, void* dx, void* dz, float* dweight, float* dbias,
+                          const gdn_norm_problem_t* prob, void* workspace, size_t workspace_bytes,
+                          void* stream);
 
 /* Debug check of the device-array preconditions: cu_seqlens[0] == 0, non-decreasing,
  * cu_seqlens[B] == N; cache_indices distinct and in [0, pool). Copies both arrays to
