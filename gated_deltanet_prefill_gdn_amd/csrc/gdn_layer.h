@@ -147,7 +147,8 @@ struct SsmShape {
   bool bf16;
 };
 size_t ssm_workspace(const SsmShape& s);
-bool ssm_grids_fit(const SsmShape& s, bool decode);
+bool ssm_prefill_grids_fit(const SsmShape& s);
+bool ssm_decode_grid_fits(const SsmShape& s);
 hipError_t launch_ssm_prefill(const SsmShape& s, const void* C, const void* B, const void* x,
                               const float* dt, const float* A_log, const float* dt_bias,
                               const float* D, float* state, const int64_t* idx,

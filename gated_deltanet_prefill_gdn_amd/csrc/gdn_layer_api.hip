@@ -195,7 +195,7 @@ gdn_status_t gdn_ssm_prefill_fwd(const void* C, const void* B, const void* x, co
     return GDN_ERR_INVALID_ARG;
   for (const void* p : {C, B, x, (const void*)out, (const void*)state_pool})
     if (!aligned16(p)) return GDN_ERR_INVALID_ARG;
-  if (!ssm_grids_fit(s, false)) return GDN_ERR_UNSUPPORTED;
+  if (!ssm_prefill_grids_fit(s)) return GDN_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < ssm_workspace(s) || ((uintptr_t)workspace & 255) != 0)
     return GDN_ERR_WORKSPACE;
   const hipError_t e = launch_ssm_prefill(s, C, B, x, dt, A_log, dt_bias, D, state_pool,
@@ -217,7 +217,7 @@ gdn_status_t gdn_ssm_decode_fwd(const void* C, const void* B, const void* x, con
     return GDN_ERR_INVALID_ARG;
   for (const void* p : {C, B, x, (const void*)out, (const void*)state_pool})
     if (!aligned16(p)) return GDN_ERR_INVALID_ARG;
-  if (!ssm_grids_fit(s, true)) return GDN_ERR_UNSUPPORTED;
+  if (!ssm_decode_grid_fits(s)) return GDN_ERR_UNSUPPORTED;
   const hipError_t e = launch_ssm_decode(s, C, B, x, dt, A_log, dt_bias, D, state_pool,
                                          cache_indices, out, (hipStream_t)stream);
   return e == hipSuccess ? GDN_OK : GDN_ERR_HIP;

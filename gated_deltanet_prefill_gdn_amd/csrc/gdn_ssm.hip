@@ -1,4 +1,4 @@
-// Selective state space scan, token by token.
+// One step of the selective state space scan.
 //
 //   d = softplus(dt + dt_bias),  a = exp(-exp(A_log) d),  S <- a S + d x B^T,  out = S C + D x
 //
@@ -163,16 +163,7 @@ hipError_t launch_token_any(const SsmShape& s, const void* C, const void* B, con
 
 }  // namespace
 
-size_t ssm_workspace(const SsmShape&) { return 256; }
-
-bool ssm_grids_fit(const SsmShape& s, bool) { return grid_ok(token_blocks(s), kTokenThreads); }
-
-hipError_t launch_ssm_prefill(const SsmShape& s, const void* C, const void* B, const void* x,
-                              const float* dt, const float* A_log, const float* dt_bias,
-                              const float* D, float* state, const int64_t* idx,
-                              const int64_t* cu, void* out, char*, hipStream_t st) {
-  return launch_token_any(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu, out, st);
-}
+bool ssm_decode_grid_fits(const SsmShape& s) { return grid_ok(token_blocks(s), kTokenThreads); }
 
 hipError_t launch_ssm_decode(const SsmShape& s, const void* C, const void* B, const void* x,
                              const float* dt, const float* A_log, const float* dt_bias,

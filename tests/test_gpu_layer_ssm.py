@@ -3,10 +3,12 @@
 Tolerances, derived. Let M be the same recurrence over absolute values (the oracle's magnitudes):
 any evaluation that rounds the factors of its products by a relative r is off by at most about
 r M. States are fp32 and every factor of their sums carries at least 16 bits: 2^-16 M covers the
-split factors (2^-17 each side), the gates (steps of 2^-24, exponents below 128 steps) and the
-fp32 sums. Outputs: for bf16 inputs the decayed scores and the start state enter the matrix
-products as bf16 (2^-8 each, and their own factors below that), so 2^-8 M + 2^-9 M; for fp32
-inputs split factors, 2^-15 M. Then one rounding to the output type."""
+one split factor of bf16 inputs (a pair of bf16 is 2^-17 off at most: the second part is below
+2^-8 of the value, in a binade whose steps are 2^-16) and as much again for the gates (steps of
+2^-24, exponents below 128 steps) and the fp32 sums; fp32 inputs are split in three and stay far
+below. Outputs: for bf16 inputs the decayed scores and the start state enter the matrix products
+as bf16 (2^-8 each, and their own factors below that), so 2^-8 M + 2^-9 M; for fp32 inputs
+2^-15 M. Then one rounding to the output type."""
 import numpy as np
 import pytest
 
@@ -128,20 +130,29 @@ def test_ssm_padding_requests_rows_and_nan(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_ssm_nan_stays_in_its_request_and_after(dtype):
+def test_ssm_nan_stays_in_its_request(dtype):
+    """Besides the tokens after it, a bad x reaches at most the 31 before it in its request (they
+    share a step of a matrix product, where its weight is zero); a bad B or C no token before."""
+    bad = float("nan")
     c = make(11, [100, 100, 100], 1, 1, 64, 64, dtype)
     good, gpool = call(c)
     c["x"][150, 0, 5] = float("nan")
     out, pool = call(c)
     keep = torch.ones(300, 64, dtype=torch.bool, device=DEV)
-    keep[150:200, 5] = False
-    # tokens of the same request before the NaN are not reached by it
+    keep[119:200, 5] = False
     assert torch.equal(out[:, 0][keep], good[:, 0][keep])
     assert torch.isnan(out[150:200, 0, 5]).all()
     s = c["idx"][1]
     assert torch.isnan(pool[s, 0, 5]).all()
     pool[s, 0, 5] = gpool[s, 0, 5]
     assert torch.equal(pool, gpool)
+    c["x"][150, 0, 5], c["B"][150, 0, 3], c["C"][30, 0, 1] = 0.0, bad, bad
+    c2 = dict(c, B=c["B"].clone(), C=c["C"].clone())
+    c2["B"][150, 0, 3], c2["C"][30, 0, 1] = 0.0, 0.0
+    (out, _), (good, _) = call(c), call(c2)
+    keep[:] = True
+    keep[30], keep[150:200] = False, False
+    assert torch.equal(out[:, 0][keep], good[:, 0][keep])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
