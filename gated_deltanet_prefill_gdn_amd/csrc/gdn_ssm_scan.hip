@@ -14,10 +14,11 @@
 // of one column, which is also what the next products want as an operand, so the state and the
 // scores never move between lanes.
 //
-// Requests longer than a segment are cut: a first pass forms each segment's state from zero, a
-// second joins them in order into every segment's start state, and the output pass runs all
-// segments side by side. Only the scalar decay per head lies between two segments, so the join
-// is one multiply-add per state entry and segment.
+// Requests longer than a segment are cut: a first launch forms each segment's state from zero (and
+// takes the requests that are not cut from start to end), a second joins the segments' states in
+// order into their start states and the final one, and a third forms the outputs of all segments
+// of cut requests side by side. Only the scalar decay per head lies between two segments, so the
+// join is one multiply-add per state entry and segment.
 //
 // Precision: bf16 inputs enter the products as they are. The decayed x of the state's update are
 // pairs of bf16 (hi + lo, at most 2^-17 off), since states are fp32 results; the decayed scores
@@ -26,6 +27,8 @@
 // of parts that reach 2^-24: 2.7 times the rate of the fp32 matrix instructions.
 // Gates and their sums are fp32 (the sums of fp32 inputs fp64), and exponents are only taken of
 // differences that are not positive, so strong decays underflow to zero and nothing overflows.
+#include <type_traits>
+
 #include "gdn_layer.h"
 #include "gdn_mfma.h"
 
@@ -43,7 +46,6 @@ typedef mfma::f32x4 acc4;
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kColsWave = 32, kColsBlock = kColsWave * kWaves;  // value columns
-constexpr int kPad = 8;  // bf16 entries between LDS rows: the rows of a fragment in other banks
 
 struct ScanArgs {
   const void *C, *B, *x;
@@ -126,8 +128,18 @@ __device__ __forceinline__ bool find_segment(const ScanArgs& a, int seg, Segment
   return s.t0 < s.t1 && slot >= 0 && slot < a.npool;
 }
 
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// 2^x in one instruction (one step off; results below 2^-126 are zero). The logs of the decays
+// are kept to base 2.
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// log(1 + e^x) = max(x, 0) + log1p(z), z = e^-|x|: with w = 1 + z rounded, log1p(z) is
+// log(w) z / (w - 1), in which the rounding of w cancels, and z where w is 1.
 __device__ __forceinline__ float softplusf(float x) {
-  return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
+  const float z = exp2_(-fabsf(x) * kLog2e), w = 1.f + z;
+  const float l = __builtin_amdgcn_logf(w) * (z * __builtin_amdgcn_rcpf((w - 1.f) * kLog2e));
+  return fmaxf(x, 0.f) + (w == 1.f ? z : l);
 }
 
 // v as a sum of P bf16: 2^-8, 2^-17 or 2^-25 of v off.
@@ -140,33 +152,53 @@ __device__ __forceinline__ void split(float v, __bf16 (&part)[P]) {
   }
 }
 
-// Running sums over the wave's lanes, inclusive from the front, exclusive from the back.
+// v from another lane of the same row of 16, chosen by a DPP control code; 0 from outside it.
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  const i32x2 b = __builtin_bit_cast(i32x2, v);
+  return __builtin_bit_cast(double, i32x2{dpp<CTRL>(b[0]), dpp<CTRL>(b[1])});
+}
+// Sum over this lane and those before it in its row of 16 lanes.
 template <typename R>
-__device__ __forceinline__ R prefix(R v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const R y = __shfl_up(v, off, 64);
-    if (lane >= off) v += y;
-  }
+__device__ __forceinline__ R row_prefix(R v) {
+  v += dpp<0x111>(v);  // from 1, 2, 4, 8 lanes before
+  v += dpp<0x112>(v);
+  v += dpp<0x114>(v);
+  v += dpp<0x118>(v);
   return v;
 }
-__device__ __forceinline__ float suffix_exclusive(float g) {
-  const int lane = threadIdx.x & 63;
-  float v = __shfl_down(g, 1, 64);
-  if (lane == 63) v = 0.f;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const float y = __shfl_down(v, off, 64);
-    if (lane + off < 64) v += y;
-  }
+// Sum over the lanes behind this one in its row.
+__device__ __forceinline__ float row_behind(float v) {
+  v = dpp<0x101>(v);  // from 1, 2, 4, 8 lanes behind
+  v += dpp<0x101>(v);
+  v += dpp<0x102>(v);
+  v += dpp<0x104>(v);
+  v += dpp<0x108>(v);
   return v;
+}
+__device__ __forceinline__ float lane_of(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+__device__ __forceinline__ double lane_of(double v, int lane) {
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  const i32x2 b = __builtin_bit_cast(i32x2, v);
+  return __builtin_bit_cast(double, i32x2{__builtin_amdgcn_readlane(b[0], lane),
+                                          __builtin_amdgcn_readlane(b[1], lane)});
 }
 
 // What a wave knows of a chunk's gates, one entry per token (its own head's).
 template <int CH, typename R>
 struct Gates {
-  R G[CH];             // running sum of g in the chunk
+  R G[CH];             // running sum of g in the chunk (to base 2, as every sum of g here)
   float step[CH];      // d
   float eG[CH];        // e^G
   float row[CH];       // e^{G_t - G at the start of t's tile}
@@ -186,24 +218,32 @@ __device__ __forceinline__ bfrag frag_col(const __bf16* tile, int ld, int col0, 
       mfma::col_frag_tr(reinterpret_cast<const uint16_t*>(tile), ld, col0, s, g, m));
 }
 
+// The rows of a chunk seen through a buffer descriptor: a lane's byte offset stays the same from
+// chunk to chunk, and rows behind the segment's end read as zero and drop what is stored to them
+// (the offset of such a row is at least (rows - 1) ld + cols, the descriptor's size).
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t chunk_rows(const void* base, int64_t ld_bytes, int rows,
+                                             int col_bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0,
+                                           (int)((rows - 1) * ld_bytes) + col_bytes, 0x00020000);
+}
+
 // Staging of a tile of CH rows x COLS entries: 16-byte pieces in registers between the load and
 // the LDS store, so that the next chunk's rows travel while this one is worked on.
 template <typename T, int CH, int COLS>
 struct Stage {
   static constexpr int V = 16 / (int)sizeof(T);
   static constexpr int PER_ROW = COLS / V, PIECES = CH * PER_ROW / kThreads;
-  static_assert(CH * PER_ROW % kThreads == 0, "whole pieces per thread");
+  static constexpr int ROWS = kThreads / PER_ROW;  // rows of one piece of all threads
+  static_assert(CH * PER_ROW % kThreads == 0 && kThreads % PER_ROW == 0, "whole rows at a time");
   u32x4 r[PIECES];
-  // rows t0 .. t0 + CH - 1 of a matrix with row stride ld; rows from t1 on, and columns from
-  // `cols` on, read as zero
-  __device__ __forceinline__ void load(const T* base, int64_t ld, int64_t t0, int64_t t1, int cols) {
+  __device__ __forceinline__ void load(const T* base, int64_t ld, int rows, int cols) {
+    const int ldb = (int)(ld * (int)sizeof(T));
+    const rsrc_t q = chunk_rows(base, ldb, rows, cols * (int)sizeof(T));
+    const int at = (int)(threadIdx.x / PER_ROW) * ldb + (int)(threadIdx.x % PER_ROW) * 16;
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      const int p = i * kThreads + threadIdx.x, row = p / PER_ROW, c = p % PER_ROW * V;
-      r[i] = u32x4{0, 0, 0, 0};
-      if (t0 + row < t1 && c < cols)
-        r[i] = *reinterpret_cast<const u32x4*>(base + (t0 + row) * ld + c);
-    }
+    for (int i = 0; i < PIECES; ++i)
+      r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(q, at + i * ROWS * ldb, 0, 0));
   }
   // as NP tiles of bf16 parts, `plane` entries apart
   template <int NP>
@@ -237,36 +277,48 @@ __device__ __forceinline__ void triangle(int i, int& tt, int& jt) {
   jt = i - tt * (tt + 1) / 2;
 }
 
-// OUT: the output pass. Otherwise the pass that forms each segment's state from zero.
-template <typename T, int DK, int CH, bool OUT>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kernel(ScanArgs a) {
-  constexpr bool F32 = sizeof(T) == 4;
-  constexpr int NP = F32 ? 3 : 1;               // bf16 parts of an input, scores and S in S C
-  constexpr int NU = F32 ? 3 : 2;               // ... of the update's decayed x
+// What a workgroup does with its segment: a whole request, outputs and state; the state of a
+// piece from zero; the outputs of a piece from its start state.
+enum Mode { kWhole, kState, kOutput };
+
+template <typename T, int DK, int CH>
+struct Dims {
+  static constexpr int NP = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of an input, scores and S in S C
+  // LDS rows: 16 rows read across at once fall into different banks (C: 8-byte pieces of 16 rows;
+  // B and x: transposed reads of 8-byte pieces of 8 rows)
+  static constexpr int LDC = DK + 8, LDB = DK + 16, LDX = kColsBlock + 16, LDR = CH + 4;
+  static constexpr int TileC = CH * LDC, TileB = CH * LDB, TileX = CH * LDX;
+  using R = typename std::conditional<sizeof(T) == 4, double, float>::type;
+  using G = Gates<CH, R>;
+  // LDS: B, x, gates; with outputs also C and the scores
+  static constexpr int AtX = NP * TileB * 2, AtG = AtX + NP * TileX * 2;
+  static constexpr int AtC = AtG + kWaves * (int)sizeof(G), AtRaw = AtC + NP * TileC * 2;
+  static constexpr int Bytes = AtRaw + CH * LDR * 4;
+  static_assert(AtX % 16 == 0 && AtG % 16 == 0 && AtC % 16 == 0 && AtRaw % 16 == 0, "16-byte rows");
+};
+
+template <typename T, int DK, int CH, Mode MODE>
+__device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& sg, int in_seg,
+                                             char* lds) {
+  using D = Dims<T, DK, CH>;
+  using R = typename D::R;
+  using G = typename D::G;
+  constexpr bool F32 = sizeof(T) == 4, OUT = MODE != kState;
+  constexpr int NP = D::NP;
+  // ... of the update's decayed x: the state of a piece's outputs is only read by S C
+  constexpr int NU = F32 ? 3 : MODE == kOutput ? 1 : 2;
   constexpr int NT = CH / 16, NK = CH / 32;      // token tiles, k steps over tokens
   constexpr int NS = DK / 16, NKS = DK / 32;     // state tiles, k steps over state entries
-  constexpr int LDB = DK + kPad, LDX = kColsBlock + kPad, LDR = CH + 4;
   constexpr int NTRI = NT * (NT + 1) / 2, TRI = (NTRI + kWaves - 1) / kWaves;
-  using R = typename std::conditional<F32, double, float>::type;
-  using G = Gates<CH, R>;
+  constexpr int LDC = D::LDC, LDB = D::LDB, LDX = D::LDX, LDR = D::LDR;
+  constexpr int kTileC = D::TileC, kTileB = D::TileB, kTileX = D::TileX;
+  __bf16* const s_b = reinterpret_cast<__bf16*>(lds);
+  __bf16* const s_x = reinterpret_cast<__bf16*>(lds + D::AtX);
+  G* const s_g = reinterpret_cast<G*>(lds + D::AtG);
+  __bf16* const s_c = reinterpret_cast<__bf16*>(lds + D::AtC);
+  float* const raw = reinterpret_cast<float*>(lds + D::AtRaw);  // scores, row t, entry j
 
-  constexpr int kTileB = CH * LDB, kTileX = CH * LDX;
-  // the scores take C's place once S C has been formed
-  constexpr int kC = !OUT ? 0 : kTileB * NP * 2 > CH * LDR * 4 ? kTileB * NP * 2 : CH * LDR * 4;
-  __shared__ __align__(16) char s_c[kC + 16];
-  __shared__ __align__(16) __bf16 s_b[NP * kTileB];
-  __shared__ __align__(16) __bf16 s_x[NP * kTileX];
-  __shared__ G s_g[kWaves];
-  __bf16* const tc = reinterpret_cast<__bf16*>(s_c);
-  float* const raw = reinterpret_cast<float*>(s_c);
-
-  const int blk = blockIdx.x;
-  const int per_seg = a.H * a.blocks_per_group;
-  Segment sg;
-  if (!find_segment(a, blk / per_seg, sg)) return;
-  const bool last = sg.index + 1 == sg.count;
-  if (!OUT && last) return;  // nothing starts from it
-  const int in_seg = blk % per_seg, h = in_seg / a.blocks_per_group;
+  const int h = in_seg / a.blocks_per_group;
   const int col0 = in_seg % a.blocks_per_group * kColsBlock;  // of the group's columns
   const int vc = a.rep * a.dv;
   const int ncols = vc - col0 < kColsBlock ? vc - col0 : kColsBlock;
@@ -281,6 +333,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void ssm_scan_ker
   const T* const gB = reinterpret_cast<const T*>(a.B) + (int64_t)h * DK;
   const T* const gC = reinterpret_cast<const T*>(a.C) + (int64_t)h * DK;
   const T* const gx = reinterpret_cast<const T*>(a.x) + (int64_t)h * vc + col0;
+  T* const gout = reinterpret_cast<T*>(a.out) + (int64_t)hv * a.dv + p0;
   const int64_t ldb = (int64_t)a.H * DK, ldx = (int64_t)a.HV * a.dv;
 
   // S^T: st[s tile][column tile], entries 16 s + 4 g .. + 3 of column p0 + 16 pt + r
@@ -288,7 +341,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void ssm_scan_ker
   const float* from = nullptr;
   const int64_t plane = (int64_t)a.dv * DK;
   if (OUT) {
-    from = sg.count > 1 ? a.seg_state + ((int64_t)sg.ws * a.HV + hv) * plane
+    from = MODE == kOutput ? a.seg_state + ((int64_t)sg.ws * a.HV + hv) * plane
                         : a.pool + (slot * a.HV + hv) * plane;
     from += (int64_t)(p0 + r) * DK + 4 * g;
   }
@@ -299,7 +352,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void ssm_scan_ker
       st[s][pt] = OUT && live ? *reinterpret_cast<const acc4*>(from + 16 * pt * DK + 16 * s)
                               : acc4{0.f, 0.f, 0.f, 0.f};
 
-  const float decay = -expf(a.A_log[hv]), dtb = a.dt_bias[hv];
+  const float decay = -expf(a.A_log[hv]) * kLog2e, dtb = a.dt_bias[hv];
   const float dskip = a.D ? a.D[hv] : 0.f;
   float gsum = 0.f;  // of g over the segment
 
@@ -307,48 +360,56 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void ssm_scan_ker
   Stage<T, CH, kColsBlock> qx;
   float qdt = 0.f;
   auto fetch = [&](int64_t t) {
-    qb.load(gB, ldb, t, sg.t1, DK);
-    if constexpr (OUT) qc.load(gC, ldb, t, sg.t1, DK);
-    qx.load(gx, ldx, t, sg.t1, ncols);
-    qdt = lane < CH && t + lane < sg.t1 ? a.dt[(t + lane) * a.HV + hv] : 0.f;
+    const int rows = sg.t1 - t < CH ? (int)(sg.t1 - t) : CH;
+    qb.load(gB + t * ldb, ldb, rows, DK);
+    if constexpr (OUT) qc.load(gC + t * ldb, ldb, rows, DK);
+    qx.load(gx + t * ldx, ldx, rows, ncols);
+    qdt = __builtin_bit_cast(
+        float, __builtin_amdgcn_raw_buffer_load_b32(
+                   chunk_rows(a.dt + t * a.HV + hv, (int64_t)a.HV * 4, rows, 4), lane * a.HV * 4, 0, 0));
   };
   fetch(sg.t0);
 
   for (int64_t t0 = sg.t0; t0 < sg.t1; t0 += CH) {
     if (t0 > sg.t0) __syncthreads();  // the chunk before has been read
+    const int rows = sg.t1 - t0 < CH ? (int)(sg.t1 - t0) : CH;
     qb.template store<NP>(s_b, kTileB, LDB);
-    if constexpr (OUT) qc.template store<NP>(tc, kTileB, LDB);
+    if constexpr (OUT) qc.template store<NP>(s_c, kTileC, LDC);
     qx.template store<NP>(s_x, kTileX, LDX);
     G& gt = s_g[wv];
     float eGn;
     {  // gates, a lane per token; rows past the end have no step and no decay
-      const bool in = lane < CH && t0 + lane < sg.t1;
+      const bool in = lane < rows;
       const float step = in ? softplusf(qdt + dtb) : 0.f;
       const float gl = in ? decay * step : 0.f;
-      const R Gp = prefix<R>((R)gl);
-      const float rest = suffix_exclusive(gl);
-      const float tot = (float)__shfl(Gp, 63, 64);
-      eGn = expf(tot);
-      gsum += tot;
-      if constexpr (OUT) {
-        R at[NT];  // G before each tile
-        at[0] = 0;
+      const R local = row_prefix((R)gl);
+      R at[NT + 1];  // G before each tile, and at the end
+      at[0] = 0;
 #pragma unroll
-        for (int k = 1; k < NT; ++k) at[k] = __shfl(Gp, 16 * k - 1, 64);
-        if (lane < CH) {
+      for (int k = 0; k < NT; ++k) at[k + 1] = at[k] + lane_of(local, 16 * k + 15);
+      float after = 0.f;  // of g in the tiles behind this lane's
+      R mine = at[0];
+#pragma unroll
+      for (int k = NT - 1; k > 0; --k)
+        after += lane < 16 * k ? lane_of((float)local, 16 * k + 15) : 0.f;
+#pragma unroll
+      for (int k = 1; k < NT; ++k) mine = lane >= 16 * k ? at[k] : mine;
+      const float tot = (float)at[NT];
+      eGn = exp2_(tot);
+      gsum += tot;
+      if (lane < CH) {
+        if constexpr (OUT) {
+          const R Gp = mine + local;
           gt.G[lane] = Gp;
           gt.step[lane] = step;
-          gt.eG[lane] = expf((float)Gp);
-          R mine = at[0];
+          gt.eG[lane] = exp2_((float)Gp);
+          gt.row[lane] = exp2_((float)local);
 #pragma unroll
-          for (int k = 1; k < NT; ++k) {
-            if (lane / 16 == k) mine = at[k];
-            gt.col[k][lane] = lane < 16 * k ? step * expf((float)(at[k] - Gp)) : 0.f;
-          }
-          gt.row[lane] = expf((float)(Gp - mine));
+          for (int k = 1; k < NT; ++k)
+            gt.col[k][lane] = lane < 16 * k ? step * exp2_((float)(at[k] - Gp)) : 0.f;
         }
+        gt.w[lane] = step * exp2_(row_behind(gl) + after);
       }
-      if (lane < CH) gt.w[lane] = step * expf(rest);
     }
     __syncthreads();
     if (t0 + CH < sg.t1) fetch(t0 + CH);
@@ -363,15 +424,32 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void ssm_scan_ker
           xf[p][pt][k] = frag_col(s_x + p * kTileX, LDX, kColsWave * wv + 16 * pt, k, g, r);
 
     if constexpr (OUT) {
-      // Y^T = e^G (S C^T): y[t tile][column tile], columns 4 g .. + 3 of token 16 t + r
-      acc4 y[NT][2];
+      // scores^T, j x t, shared by the workgroup's heads: each wave some of the tiles
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int i = 0; i < TRI; ++i) {
+        const int n = wv + i * kWaves;
+        if (n >= NTRI) continue;
+        int tt, jt;
+        triangle(n, tt, jt);
+        acc4 sc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt) y[t][pt] = acc4{0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < NKS; ++k)
 #pragma unroll
-      for (int k = 0; k < NKS; ++k) {
-        bfrag sb[NP][2];
+          for (int p = 0; p < NP; ++p) {
+            const bfrag c = *reinterpret_cast<const bfrag*>(
+                s_c + p * kTileC + (16 * tt + r) * LDC + 32 * k + 8 * g);
+#pragma unroll
+            for (int q = 0; q + p < NP; ++q) {
+              const bfrag b = *reinterpret_cast<const bfrag*>(
+                  s_b + q * kTileB + (16 * jt + r) * LDB + 32 * k + 8 * g);
+              sc = mma_bf16(b, c, sc);
+            }
+          }
+        *reinterpret_cast<acc4*>(raw + (16 * tt + r) * LDR + 16 * jt + 4 * g) = sc;
+      }
+      bfrag sb[NP][2][NKS];  // S^T as the operand of S C
+#pragma unroll
+      for (int k = 0; k < NKS; ++k)
 #pragma unroll
         for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
@@ -379,61 +457,31 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void ssm_scan_ker
             __bf16 part[NP];
             split<NP>(st[2 * k + e / 4][pt][e % 4], part);
 #pragma unroll
-            for (int p = 0; p < NP; ++p) sb[p][pt][e] = part[p];
+            for (int p = 0; p < NP; ++p) sb[p][pt][k][e] = part[p];
           }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            const bfrag c = frag_kperm(tc + p * kTileB + (16 * t + r) * LDB + 32 * k, g);
-#pragma unroll
-            for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-              for (int q = 0; q + p < NP; ++q) y[t][pt] = mma_bf16(sb[q][pt], c, y[t][pt]);
-          }
-      }
-      // scores^T, j x t, shared by the workgroup's heads: each wave some of the tiles
-      acc4 sc[TRI];
-#pragma unroll
-      for (int i = 0; i < TRI; ++i) {
-        sc[i] = acc4{0.f, 0.f, 0.f, 0.f};
-        const int n = wv + i * kWaves;
-        if (n >= NTRI) continue;
-        int tt, jt;
-        triangle(n, tt, jt);
+      __syncthreads();
+      // Y^T tile by tile: columns 16 pt + 4 g .. + 3 of token 16 t + r
+      const rsrc_t qo = chunk_rows(gout + t0 * ldx, ldx * (int)sizeof(T), rows, kColsWave * (int)sizeof(T));
+#pragma unroll 1
+      for (int t = 0; t < NT; ++t) {
+        acc4 y[2] = {acc4{0.f, 0.f, 0.f, 0.f}, acc4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int k = 0; k < NKS; ++k)
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            const bfrag c = *reinterpret_cast<const bfrag*>(
-                tc + p * kTileB + (16 * tt + r) * LDB + 32 * k + 8 * g);
+            const bfrag c = frag_kperm(s_c + p * kTileC + (16 * t + r) * LDC + 32 * k, g);
 #pragma unroll
-            for (int q = 0; q + p < NP; ++q) {
-              const bfrag b = *reinterpret_cast<const bfrag*>(
-                  s_b + q * kTileB + (16 * jt + r) * LDB + 32 * k + 8 * g);
-              sc[i] = mma_bf16(b, c, sc[i]);
-            }
+            for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+              for (int q = 0; q + p < NP; ++q) y[pt] = mma_bf16(sb[q][pt][k], c, y[pt]);
           }
-      }
-      __syncthreads();  // C has been read
-#pragma unroll
-      for (int i = 0; i < TRI; ++i) {
-        const int n = wv + i * kWaves;
-        if (n >= NTRI) continue;
-        int tt, jt;
-        triangle(n, tt, jt);
-        *reinterpret_cast<acc4*>(raw + (16 * tt + r) * LDR + 16 * jt + 4 * g) = sc[i];
-      }
-      __syncthreads();
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
         const float e = gt.eG[16 * t + r], row = gt.row[16 * t + r];
         const R Gt = gt.G[16 * t + r];
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt) y[t][pt] *= e;
+        for (int pt = 0; pt < 2; ++pt) y[pt] *= e;
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
-          if (2 * k > t) continue;
+          if (2 * k > t) break;
           bfrag pf[NP];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -446,10 +494,10 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void ssm_scan_ker
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = s[i] * (c[i] * row);
               } else {
+                const acc4 d = *reinterpret_cast<const acc4*>(&gt.step[16 * j + 4 * g]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const int jj = 16 * j + 4 * g + i;
-                  const float ex = expf((float)(Gt - gt.G[jj])) * gt.step[jj];
+                  const float ex = exp2_((float)(Gt - gt.G[16 * j + 4 * g + i])) * d[i];
                   v[i] = 4 * g + i <= r ? s[i] * ex : 0.f;
                 }
               }
@@ -468,11 +516,10 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void ssm_scan_ker
             for (int p = 0; p < NP; ++p)
 #pragma unroll
               for (int q = 0; q + p < NP; ++q)
-                y[t][pt] = mma_bf16(xf[p][pt][k], pf[q], y[t][pt]);
+                y[pt] = mma_bf16(xf[p][pt][k], pf[q], y[pt]);
         }
         // + D x, and out: four columns of one token per lane
-        const int64_t tok = t0 + 16 * t + r;
-        if (live && tok < sg.t1) {
+        if (live) {
 #pragma unroll
           for (int pt = 0; pt < 2; ++pt) {
             const int at = (16 * t + r) * LDX + kColsWave * wv + 16 * pt + 4 * g;
@@ -482,15 +529,16 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void ssm_scan_ker
               float xv = 0.f;
 #pragma unroll
               for (int p = NP - 1; p >= 0; --p) xv += (float)s_x[p * kTileX + at + i];
-              o[i] = __builtin_fmaf(dskip, xv, y[t][pt][i]);
+              o[i] = __builtin_fmaf(dskip, xv, y[pt][i]);
             }
-            T* const dst = reinterpret_cast<T*>(a.out) + tok * ldx + (int64_t)hv * a.dv + p0 +
-                           16 * pt + 4 * g;
+            const int to = (16 * t + r) * (int)(ldx * sizeof(T)) + (16 * pt + 4 * g) * (int)sizeof(T);
             if constexpr (F32) {
-              *reinterpret_cast<f32x4*>(dst) = f32x4{o[0], o[1], o[2], o[3]};
+              __builtin_amdgcn_raw_buffer_store_b128(
+                  __builtin_bit_cast(u32x4, f32x4{o[0], o[1], o[2], o[3]}), qo, to, 0, 0);
             } else {
-              *reinterpret_cast<bf16x4*>(dst) =
-                  bf16x4{(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
+              __builtin_amdgcn_raw_buffer_store_b64(
+                  __builtin_bit_cast(u32x2, bf16x4{(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]}),
+                  qo, to, 0, 0);
             }
           }
         }
@@ -498,21 +546,24 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void ssm_scan_ker
     }
 
     // S^T <- e^{G_n} S^T + B^T (w x)
+    if (MODE == kOutput && t0 + CH >= sg.t1) break;  // nobody reads this state
     bfrag xw[NU][2][NK];
 #pragma unroll
-    for (int pt = 0; pt < 2; ++pt)
+    for (int k = 0; k < NK; ++k)
 #pragma unroll
-      for (int k = 0; k < NK; ++k)
+      for (int e = 0; e < 8; ++e) {
+        const float w = gt.w[32 * k + kperm(g, e)];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int pt = 0; pt < 2; ++pt) {
           float v = 0.f;
 #pragma unroll
           for (int p = NP - 1; p >= 0; --p) v += (float)xf[p][pt][k][e];
           __bf16 part[NU];
-          split<NU>(v * gt.w[32 * k + kperm(g, e)], part);
+          split<NU>(v * w, part);
 #pragma unroll
           for (int p = 0; p < NU; ++p) xw[p][pt][k][e] = part[p];
         }
+      }
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
 #pragma unroll
@@ -525,26 +576,42 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void ssm_scan_ker
 #pragma unroll
           for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
-            for (int q = 0; q + p < NU; ++q)
-              // pieces of a cut request but its last: their state is only read by S C above
-              if (q == 0 || !OUT || F32 || last) st[s][pt] = mma_bf16(b, xw[q][pt][k], st[s][pt]);
+            for (int q = 0; q + p < NU; ++q) st[s][pt] = mma_bf16(b, xw[q][pt][k], st[s][pt]);
         }
     }
   }
 
-  if (!live || (OUT && !last)) return;
-  float* to = OUT ? a.pool + (slot * a.HV + hv) * plane
-                  : a.seg_state + ((int64_t)sg.ws * a.HV + hv) * plane;
+  if (!live || MODE == kOutput) return;
+  float* to = MODE == kWhole ? a.pool + (slot * a.HV + hv) * plane
+                             : a.seg_state + ((int64_t)sg.ws * a.HV + hv) * plane;
   to += (int64_t)(p0 + r) * DK + 4 * g;
 #pragma unroll
   for (int s = 0; s < NS; ++s)
 #pragma unroll
     for (int pt = 0; pt < 2; ++pt)
       *reinterpret_cast<acc4*>(to + 16 * pt * DK + 16 * s) = st[s][pt];
-  if (!OUT && p0 == 0 && lane == 0) a.seg_decay[(int64_t)sg.ws * a.HV + hv] = gsum;
+  if (MODE == kState && p0 == 0 && lane == 0) a.seg_decay[(int64_t)sg.ws * a.HV + hv] = gsum;
 }
 
-// Start states of a cut request's segments, in place of the segments' own states.
+// The first launch (OUTPUT false): whole requests, and the states of cut ones' pieces. The last:
+// the outputs of cut requests.
+template <typename T, int DK, int CH, bool OUTPUT>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DK < 256 ? 2 : 1) void ssm_scan_kernel(ScanArgs a) {
+  __shared__ __align__(16) char lds[Dims<T, DK, CH>::Bytes];
+  const int per_seg = a.H * a.blocks_per_group;
+  const int seg = blockIdx.x / per_seg, in_seg = blockIdx.x % per_seg;
+  Segment sg;
+  if (!find_segment(a, seg, sg)) return;
+  if constexpr (OUTPUT) {
+    if (sg.count > 1) scan_segment<T, DK, CH, kOutput>(a, sg, in_seg, lds);
+  } else if (sg.count > 1) {
+    scan_segment<T, DK, CH, kState>(a, sg, in_seg, lds);
+  } else {
+    scan_segment<T, DK, CH, kWhole>(a, sg, in_seg, lds);
+  }
+}
+
+// Start states of a cut request's pieces, in place of the pieces' own states, and its final state.
 __global__ __launch_bounds__(256) void ssm_join_kernel(ScanArgs a, int plane, int parts) {
   const int part = blockIdx.x % parts;
   const int64_t pair = blockIdx.x / parts;
@@ -561,20 +628,17 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(ScanArgs a, int plane, in
   }
   const int e = (part * 256 + threadIdx.x) * 4;
   if (first + n > a.max_cut) return;
-  f32x4 s = *reinterpret_cast<const f32x4*>(a.pool + (slot * a.HV + hv) * (int64_t)plane + e);
+  f32x4* const home = reinterpret_cast<f32x4*>(a.pool + (slot * a.HV + hv) * (int64_t)plane + e);
+  f32x4 s = *home;
   float* p = a.seg_state + ((int64_t)first * a.HV + hv) * plane + e;
   const float* d = a.seg_decay + (int64_t)first * a.HV + hv;
   const int64_t step = (int64_t)a.HV * plane;
   for (int i = 0; i < n; ++i, p += step, d += a.HV) {
-    f32x4 mine = {0.f, 0.f, 0.f, 0.f};
-    float f = 0.f;
-    if (i + 1 < n) {
-      mine = *reinterpret_cast<const f32x4*>(p);
-      f = expf(*d);
-    }
+    const f32x4 mine = *reinterpret_cast<const f32x4*>(p);
     *reinterpret_cast<f32x4*>(p) = s;
-    s = s * f + mine;
+    s = s * exp2_(*d) + mine;
   }
+  *home = s;
 }
 
 // Tokens of a segment: enough segments to fill the device, each long enough that the state it
@@ -611,16 +675,17 @@ int64_t scan_blocks(const SsmShape& s) {
 template <typename T, int DK, int CH>
 hipError_t launch_scan(const SsmShape& s, const ScanArgs& a, hipStream_t st) {
   const unsigned blocks = (unsigned)scan_blocks(s);
+  hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, false>), dim3(blocks), dim3(kThreads), 0, st, a);
+  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (a.lseg) {
-    hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, false>), dim3(blocks), dim3(kThreads), 0, st, a);
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int parts = s.dv * s.dk / 1024;
     hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)(s.B * s.HV * parts)), dim3(256), 0, st, a,
                        s.dv * s.dk, parts);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, true>), dim3(blocks), dim3(kThreads), 0, st, a);
+    return hipGetLastError();
   }
-  hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, true>), dim3(blocks), dim3(kThreads), 0, st, a);
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace
@@ -628,7 +693,10 @@ hipError_t launch_scan(const SsmShape& s, const ScanArgs& a, hipStream_t st) {
 size_t ssm_workspace(const SsmShape& s) { return scan_layout(s).total; }
 
 bool ssm_prefill_grids_fit(const SsmShape& s) {
-  return grid_ok(scan_blocks(s), kThreads) && grid_ok(s.B * s.HV * (s.dv * s.dk / 1024), 256);
+  // the byte offsets inside a chunk's rows are 32-bit
+  const int64_t row = (s.HV * (int64_t)s.dv > s.H * (int64_t)s.dk ? s.HV * (int64_t)s.dv
+                                                                  : s.H * (int64_t)s.dk) * 4;
+  return row * 64 <= 0x7FFFFFFF && grid_ok(scan_blocks(s), kThreads) && grid_ok(s.B * s.HV * (s.dv * s.dk / 1024), 256);
 }
 
 hipError_t launch_ssm_prefill(const SsmShape& s, const void* C, const void* B, const void* x,
