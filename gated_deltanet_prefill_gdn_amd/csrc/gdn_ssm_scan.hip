@@ -252,7 +252,9 @@ struct Stage {
     for (int i = 0; i < PIECES; ++i) {
       const int p = i * kThreads + threadIdx.x, row = p / PER_ROW, c = p % PER_ROW * V;
       if constexpr (NP == 1) {
-        *reinterpret_cast<u32x4*>(to + row * ld + c) = r[i];
+        u32x2* const q = reinterpret_cast<u32x2*>(to + row * ld + c);
+        q[0] = u32x2{r[i][0], r[i][1]};
+        q[1] = u32x2{r[i][2], r[i][3]};
       } else {
         const f32x4 v = __builtin_bit_cast(f32x4, r[i]);
         bf16x4 part[NP];
@@ -284,9 +286,10 @@ enum Mode { kWhole, kState, kOutput };
 template <typename T, int DK, int CH>
 struct Dims {
   static constexpr int NP = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of an input, scores and S in S C
-  // LDS rows: 16 rows read across at once fall into different banks (C: 8-byte pieces of 16 rows;
-  // B and x: transposed reads of 8-byte pieces of 8 rows)
-  static constexpr int LDC = DK + 8, LDB = DK + 16, LDX = kColsBlock + 16, LDR = CH + 4;
+  // LDS rows. 8-byte reads down 16 rows take 4.5 cycles where the stride is 2 mod 4 words (70
+  // here), 8 or 16 elsewhere, transposed reads 6.4 there; 16-byte reads of the scores 4.9 cycles
+  // at 72 words and 8 at 68 (measured, a wave's read).
+  static constexpr int LDC = DK + 12, LDB = DK + 12, LDX = kColsBlock + 12, LDR = CH + 8;
   static constexpr int TileC = CH * LDC, TileB = CH * LDB, TileX = CH * LDX;
   using R = typename std::conditional<sizeof(T) == 4, double, float>::type;
   using G = Gates<CH, R>;
@@ -436,14 +439,10 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
         for (int k = 0; k < NKS; ++k)
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            const bfrag c = *reinterpret_cast<const bfrag*>(
-                s_c + p * kTileC + (16 * tt + r) * LDC + 32 * k + 8 * g);
+            const bfrag c = frag_kperm(s_c + p * kTileC + (16 * tt + r) * LDC + 32 * k, g);
 #pragma unroll
-            for (int q = 0; q + p < NP; ++q) {
-              const bfrag b = *reinterpret_cast<const bfrag*>(
-                  s_b + q * kTileB + (16 * jt + r) * LDB + 32 * k + 8 * g);
-              sc = mma_bf16(b, c, sc);
-            }
+            for (int q = 0; q + p < NP; ++q)
+              sc = mma_bf16(frag_kperm(s_b + q * kTileB + (16 * jt + r) * LDB + 32 * k, g), c, sc);
           }
         *reinterpret_cast<acc4*>(raw + (16 * tt + r) * LDR + 16 * jt + 4 * g) = sc;
       }
