@@ -46,6 +46,7 @@ typedef mfma::f32x4 acc4;
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kColsWave = 32, kColsBlock = kColsWave * kWaves;  // value columns
+constexpr int kHeads = kColsBlock / 64;  // heads of a workgroup at most
 
 struct ScanArgs {
   const void *C, *B, *x;
@@ -195,7 +196,7 @@ __device__ __forceinline__ double lane_of(double v, int lane) {
                                           __builtin_amdgcn_readlane(b[1], lane)});
 }
 
-// What a wave knows of a chunk's gates, one entry per token (its own head's).
+// The gates of one head in one chunk, an entry per token.
 template <int CH, typename R>
 struct Gates {
   R G[CH];             // running sum of g in the chunk (to base 2, as every sum of g here)
@@ -203,7 +204,9 @@ struct Gates {
   float eG[CH];        // e^G
   float row[CH];       // e^{G_t - G at the start of t's tile}
   float w[CH];         // d e^{G_n - G}: weight in the state's update
-  float col[CH / 16][CH];  // [tile]: d_j e^{G at the tile's start - G_j}, j before the tile
+  float col[CH / 16][CH];  // [tile]: d_j e^{G at the tile's start - G_j}, j before the tile;
+                           // its first row, which has no use, holds G_n
+  __device__ __forceinline__ float total() const { return col[0][0]; }
 };
 
 // Eight entries of a row at k = kperm(g, 0..7), two 8-byte reads.
@@ -287,17 +290,16 @@ template <typename T, int DK, int CH>
 struct Dims {
   static constexpr int NP = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of an input, scores and S in S C
   // LDS rows. 8-byte reads down 16 rows take 4.5 cycles where the stride is 2 mod 4 words (70
-  // here), 8 or 16 elsewhere, transposed reads 6.4 there; 16-byte reads of the scores 4.9 cycles
-  // at 72 words and 8 at 68 (measured, a wave's read).
-  static constexpr int LDC = DK + 12, LDB = DK + 12, LDX = kColsBlock + 12, LDR = CH + 8;
-  static constexpr int TileC = CH * LDC, TileB = CH * LDB, TileX = CH * LDX;
+  // here), 8 or 16 elsewhere, transposed reads 6.4 there (measured, a wave's read).
+  static constexpr int LDC = DK + 12, LDB = DK + 12, LDX = kColsBlock + 12, LDP = CH + 8;
+  static constexpr int TileC = CH * LDC, TileB = CH * LDB, TileX = CH * LDX, TileP = CH * LDP;
   using R = typename std::conditional<sizeof(T) == 4, double, float>::type;
   using G = Gates<CH, R>;
-  // LDS: B, x, gates; with outputs also C and the scores
+  // LDS: B, x, four gate sets; with outputs also C and the decayed scores of up to two heads
   static constexpr int AtX = NP * TileB * 2, AtG = AtX + NP * TileX * 2;
-  static constexpr int AtC = AtG + kWaves * (int)sizeof(G), AtRaw = AtC + NP * TileC * 2;
-  static constexpr int Bytes = AtRaw + CH * LDR * 4;
-  static_assert(AtX % 16 == 0 && AtG % 16 == 0 && AtC % 16 == 0 && AtRaw % 16 == 0, "16-byte rows");
+  static constexpr int AtC = AtG + kWaves * (int)sizeof(G), AtP = AtC + NP * TileC * 2;
+  static constexpr int Bytes = AtP + kHeads * NP * TileP * 2;
+  static_assert(AtX % 16 == 0 && AtG % 16 == 0 && AtC % 16 == 0 && AtP % 16 == 0, "16-byte rows");
 };
 
 template <typename T, int DK, int CH, Mode MODE>
@@ -313,13 +315,14 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
   constexpr int NT = CH / 16, NK = CH / 32;      // token tiles, k steps over tokens
   constexpr int NS = DK / 16, NKS = DK / 32;     // state tiles, k steps over state entries
   constexpr int NTRI = NT * (NT + 1) / 2, TRI = (NTRI + kWaves - 1) / kWaves;
-  constexpr int LDC = D::LDC, LDB = D::LDB, LDX = D::LDX, LDR = D::LDR;
-  constexpr int kTileC = D::TileC, kTileB = D::TileB, kTileX = D::TileX;
+  constexpr int LDC = D::LDC, LDB = D::LDB, LDX = D::LDX, LDP = D::LDP;
+  constexpr int kTileC = D::TileC, kTileB = D::TileB, kTileX = D::TileX, kTileP = D::TileP;
   __bf16* const s_b = reinterpret_cast<__bf16*>(lds);
   __bf16* const s_x = reinterpret_cast<__bf16*>(lds + D::AtX);
   G* const s_g = reinterpret_cast<G*>(lds + D::AtG);
   __bf16* const s_c = reinterpret_cast<__bf16*>(lds + D::AtC);
-  float* const raw = reinterpret_cast<float*>(lds + D::AtRaw);  // scores, row t, entry j
+  // decayed scores, row t; entry 32 k + 8 g + e is token j = 32 k + kperm(g, e)
+  __bf16* const s_p = reinterpret_cast<__bf16*>(lds + D::AtP);
 
   const int h = in_seg / a.blocks_per_group;
   const int col0 = in_seg % a.blocks_per_group * kColsBlock;  // of the group's columns
@@ -332,6 +335,14 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
   const int wcol = live ? col0 + kColsWave * wv : col0;
   const int hv = h * a.rep + wcol / a.dv, p0 = wcol % a.dv;
   const int64_t slot = a.idx[sg.req];
+  // Heads of the workgroup, and the one this wave's columns belong to. The four gate sets hold
+  // four chunks of one head or two of two: each wave forms one set, of head gh and the chunk
+  // gc after the batch's first.
+  const int hv0 = h * a.rep + col0 / a.dv, nh = (ncols + a.dv - 1) / a.dv;
+  const int batch = nh == 2 ? 2 : 4, gh = nh == 2 ? wv >> 1 : 0, gc = nh == 2 ? wv & 1 : wv;
+  auto gate_set = [&](int head, int chunk) -> G& {
+    return s_g[nh == 2 ? 2 * head + (chunk & 1) : chunk & 3];
+  };
 
   const T* const gB = reinterpret_cast<const T*>(a.B) + (int64_t)h * DK;
   const T* const gC = reinterpret_cast<const T*>(a.C) + (int64_t)h * DK;
@@ -355,7 +366,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
       st[s][pt] = OUT && live ? *reinterpret_cast<const acc4*>(from + 16 * pt * DK + 16 * s)
                               : acc4{0.f, 0.f, 0.f, 0.f};
 
-  const float decay = -expf(a.A_log[hv]) * kLog2e, dtb = a.dt_bias[hv];
+  const float decay = -expf(a.A_log[hv0 + gh]) * kLog2e, dtb = a.dt_bias[hv0 + gh];
   const float dskip = a.D ? a.D[hv] : 0.f;
   float gsum = 0.f;  // of g over the segment
 
@@ -367,22 +378,35 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
     qb.load(gB + t * ldb, ldb, rows, DK);
     if constexpr (OUT) qc.load(gC + t * ldb, ldb, rows, DK);
     qx.load(gx + t * ldx, ldx, rows, ncols);
-    qdt = __builtin_bit_cast(
-        float, __builtin_amdgcn_raw_buffer_load_b32(
-                   chunk_rows(a.dt + t * a.HV + hv, (int64_t)a.HV * 4, rows, 4), lane * a.HV * 4, 0, 0));
+  };
+  auto fetch_dt = [&](int64_t t) {  // of this wave's set in the batch of chunks from t on
+    const int64_t left = sg.t1 - (t + gc * CH);
+    qdt = 0.f;
+    if (left > 0)
+      qdt = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(
+                     chunk_rows(a.dt + (t + gc * CH) * a.HV + hv0 + gh, (int64_t)a.HV * 4,
+                                left < CH ? (int)left : CH, 4),
+                     lane * a.HV * 4, 0, 0));
   };
   fetch(sg.t0);
+  fetch_dt(sg.t0);
+  if constexpr (OUT) {  // scores above the diagonal stay zero
+    for (int i = tid; i < kHeads * NP * kTileP / 8; i += kThreads)
+      reinterpret_cast<u32x4*>(s_p)[i] = u32x4{0, 0, 0, 0};
+  }
 
-  for (int64_t t0 = sg.t0; t0 < sg.t1; t0 += CH) {
+  int chunk = 0;
+  for (int64_t t0 = sg.t0; t0 < sg.t1; t0 += CH, ++chunk) {
     if (t0 > sg.t0) __syncthreads();  // the chunk before has been read
     const int rows = sg.t1 - t0 < CH ? (int)(sg.t1 - t0) : CH;
     qb.template store<NP>(s_b, kTileB, LDB);
     if constexpr (OUT) qc.template store<NP>(s_c, kTileC, LDC);
     qx.template store<NP>(s_x, kTileX, LDX);
-    G& gt = s_g[wv];
-    float eGn;
-    {  // gates, a lane per token; rows past the end have no step and no decay
-      const bool in = lane < rows;
+    if (chunk % batch == 0) {
+      // a gate set, a lane per token; rows past the end have no step and no decay
+      G& gt = gate_set(gh, chunk + gc);
+      const bool in = lane < CH && t0 + gc * CH + lane < sg.t1;
       const float step = in ? softplusf(qdt + dtb) : 0.f;
       const float gl = in ? decay * step : 0.f;
       const R local = row_prefix((R)gl);
@@ -397,9 +421,6 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
         after += lane < 16 * k ? lane_of((float)local, 16 * k + 15) : 0.f;
 #pragma unroll
       for (int k = 1; k < NT; ++k) mine = lane >= 16 * k ? at[k] : mine;
-      const float tot = (float)at[NT];
-      eGn = exp2_(tot);
-      gsum += tot;
       if (lane < CH) {
         if constexpr (OUT) {
           const R Gp = mine + local;
@@ -413,9 +434,13 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
         }
         gt.w[lane] = step * exp2_(row_behind(gl) + after);
       }
+      if (lane == 0) gt.col[0][0] = (float)at[NT];
+      fetch_dt(t0 + batch * CH);
     }
     __syncthreads();
     if (t0 + CH < sg.t1) fetch(t0 + CH);
+    const G& gt = gate_set(nh == 2 ? kColsWave * wv / a.dv : 0, chunk);
+    gsum += gt.total();
 
     bfrag xf[NP][2][NK];  // x, column p0 + 16 pt + r, tokens 32 k + kperm
 #pragma unroll
@@ -427,7 +452,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
           xf[p][pt][k] = frag_col(s_x + p * kTileX, LDX, kColsWave * wv + 16 * pt, k, g, r);
 
     if constexpr (OUT) {
-      // scores^T, j x t, shared by the workgroup's heads: each wave some of the tiles
+      // scores^T, j x t: each wave some of the tiles, decayed for each of the workgroup's heads
 #pragma unroll
       for (int i = 0; i < TRI; ++i) {
         const int n = wv + i * kWaves;
@@ -444,7 +469,36 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
             for (int q = 0; q + p < NP; ++q)
               sc = mma_bf16(frag_kperm(s_b + q * kTileB + (16 * jt + r) * LDB + 32 * k, g), c, sc);
           }
-        *reinterpret_cast<acc4*>(raw + (16 * tt + r) * LDR + 16 * jt + 4 * g) = sc;
+        for (int hh = 0; hh < nh; ++hh) {
+          const G& gs = gate_set(hh, chunk);
+          float v[4];
+          if (jt < tt) {
+            const acc4 c = *reinterpret_cast<const acc4*>(&gs.col[tt][16 * jt + 4 * g]);
+            const float row = gs.row[16 * tt + r];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = sc[e] * (c[e] * row);
+          } else {
+            const acc4 d = *reinterpret_cast<const acc4*>(&gs.step[16 * jt + 4 * g]);
+            const R Gt = gs.G[16 * tt + r];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float ex = exp2_((float)(Gt - gs.G[16 * jt + 4 * g + e])) * d[e];
+              v[e] = 4 * g + e <= r ? sc[e] * ex : 0.f;
+            }
+          }
+          bf16x4 part[NP];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            __bf16 one[NP];
+            split<NP>(v[e], one);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) part[p][e] = one[p];
+          }
+#pragma unroll
+          for (int p = 0; p < NP; ++p)
+            *reinterpret_cast<bf16x4*>(s_p + (hh * NP + p) * kTileP + (16 * tt + r) * LDP +
+                                       32 * (jt / 2) + 8 * g + 4 * (jt % 2)) = part[p];
+        }
       }
       bfrag sb[NP][2][NKS];  // S^T as the operand of S C
 #pragma unroll
@@ -459,85 +513,73 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
             for (int p = 0; p < NP; ++p) sb[p][pt][k][e] = part[p];
           }
       __syncthreads();
-      // Y^T tile by tile: columns 16 pt + 4 g .. + 3 of token 16 t + r
+      // Y^T, two token tiles at a time: columns 16 pt + 4 g .. + 3 of token 16 t + r
       const rsrc_t qo = chunk_rows(gout + t0 * ldx, ldx * (int)sizeof(T), rows, kColsWave * (int)sizeof(T));
+      const __bf16* const ph = s_p + (nh == 2 ? kColsWave * wv / a.dv : 0) * NP * kTileP;
 #pragma unroll 1
-      for (int t = 0; t < NT; ++t) {
-        acc4 y[2] = {acc4{0.f, 0.f, 0.f, 0.f}, acc4{0.f, 0.f, 0.f, 0.f}};
+      for (int tp = 0; tp < NK; ++tp) {
+        acc4 yc[2][2], yp[2][2];  // of S C (without its decay), of scores times x
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int pt = 0; pt < 2; ++pt) yc[u][pt] = yp[u][pt] = acc4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < NKS; ++k)
 #pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            const bfrag c = frag_kperm(s_c + p * kTileC + (16 * t + r) * LDC + 32 * k, g);
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int pt = 0; pt < 2; ++pt)
+            for (int p = 0; p < NP; ++p) {
+              const bfrag c =
+                  frag_kperm(s_c + p * kTileC + (16 * (2 * tp + u) + r) * LDC + 32 * k, g);
 #pragma unroll
-              for (int q = 0; q + p < NP; ++q) y[pt] = mma_bf16(sb[q][pt][k], c, y[pt]);
-          }
-        const float e = gt.eG[16 * t + r], row = gt.row[16 * t + r];
-        const R Gt = gt.G[16 * t + r];
+              for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt) y[pt] *= e;
+                for (int q = 0; q + p < NP; ++q) yc[u][pt] = mma_bf16(sb[q][pt][k], c, yc[u][pt]);
+            }
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
-          if (2 * k > t) break;
-          bfrag pf[NP];
+          if (k > tp) break;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int j = 2 * k + half;  // tile of tokens j
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            if (j <= t) {
-              const acc4 s = *reinterpret_cast<const acc4*>(raw + (16 * t + r) * LDR + 16 * j + 4 * g);
-              if (j < t) {
-                const acc4 c = *reinterpret_cast<const acc4*>(&gt.col[t][16 * j + 4 * g]);
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = s[i] * (c[i] * row);
-              } else {
-                const acc4 d = *reinterpret_cast<const acc4*>(&gt.step[16 * j + 4 * g]);
+            for (int q = 0; q < NP; ++q) {
+              const bfrag pf = *reinterpret_cast<const bfrag*>(
+                  ph + q * kTileP + (16 * (2 * tp + u) + r) * LDP + 32 * k + 8 * g);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float ex = exp2_((float)(Gt - gt.G[16 * j + 4 * g + i])) * d[i];
-                  v[i] = 4 * g + i <= r ? s[i] * ex : 0.f;
-                }
-              }
+              for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+                for (int p = 0; p + q < NP; ++p) yp[u][pt] = mma_bf16(xf[p][pt][k], pf, yp[u][pt]);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              __bf16 part[NP];
-              split<NP>(v[i], part);
-#pragma unroll
-              for (int p = 0; p < NP; ++p) pf[p][4 * half + i] = part[p];
-            }
-          }
-#pragma unroll
-          for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-            for (int p = 0; p < NP; ++p)
-#pragma unroll
-              for (int q = 0; q + p < NP; ++q)
-                y[pt] = mma_bf16(xf[p][pt][k], pf[q], y[pt]);
         }
         // + D x, and out: four columns of one token per lane
         if (live) {
 #pragma unroll
-          for (int pt = 0; pt < 2; ++pt) {
-            const int at = (16 * t + r) * LDX + kColsWave * wv + 16 * pt + 4 * g;
-            float o[4];
+          for (int u = 0; u < 2; ++u) {
+            const int row = 16 * (2 * tp + u) + r;
+            const float e = gt.eG[row];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float xv = 0.f;
+            for (int pt = 0; pt < 2; ++pt) {
+              const int at = row * LDX + kColsWave * wv + 16 * pt + 4 * g;
+              float xv[4] = {0.f, 0.f, 0.f, 0.f}, o[4];
 #pragma unroll
-              for (int p = NP - 1; p >= 0; --p) xv += (float)s_x[p * kTileX + at + i];
-              o[i] = __builtin_fmaf(dskip, xv, y[pt][i]);
-            }
-            const int to = (16 * t + r) * (int)(ldx * sizeof(T)) + (16 * pt + 4 * g) * (int)sizeof(T);
-            if constexpr (F32) {
-              __builtin_amdgcn_raw_buffer_store_b128(
-                  __builtin_bit_cast(u32x4, f32x4{o[0], o[1], o[2], o[3]}), qo, to, 0, 0);
-            } else {
-              __builtin_amdgcn_raw_buffer_store_b64(
-                  __builtin_bit_cast(u32x2, bf16x4{(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]}),
-                  qo, to, 0, 0);
+              for (int p = NP - 1; p >= 0; --p) {
+                const bf16x4 xp = *reinterpret_cast<const bf16x4*>(s_x + p * kTileX + at);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xv[i] += (float)xp[i];
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                o[i] = __builtin_fmaf(e, yc[u][pt][i], __builtin_fmaf(dskip, xv[i], yp[u][pt][i]));
+              const int to = row * (int)(ldx * sizeof(T)) + (16 * pt + 4 * g) * (int)sizeof(T);
+              if constexpr (F32) {
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    __builtin_bit_cast(u32x4, f32x4{o[0], o[1], o[2], o[3]}), qo, to, 0, 0);
+              } else {
+                __builtin_amdgcn_raw_buffer_store_b64(
+                    __builtin_bit_cast(u32x2, bf16x4{(__bf16)o[0], (__bf16)o[1], (__bf16)o[2],
+                                                     (__bf16)o[3]}),
+                    qo, to, 0, 0);
+              }
             }
           }
         }
@@ -546,6 +588,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 
     // S^T <- e^{G_n} S^T + B^T (w x)
     if (MODE == kOutput && t0 + CH >= sg.t1) break;  // nobody reads this state
+    const float eGn = exp2_(gt.total());
     bfrag xw[NU][2][NK];
 #pragma unroll
     for (int k = 0; k < NK; ++k)
