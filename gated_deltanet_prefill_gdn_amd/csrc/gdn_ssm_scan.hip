@@ -204,16 +204,18 @@ struct Gates {
   float eG[CH];        // e^G
   float row[CH];       // e^{G_t - G at the start of t's tile}
   float w[CH];         // d e^{G_n - G}: weight in the state's update
-  float col[CH / 16][CH];  // [tile]: d_j e^{G at the tile's start - G_j}, j before the tile;
-                           // its first row, which has no use, holds G_n
-  __device__ __forceinline__ float total() const { return col[0][0]; }
+  float col[CH / 16 - 1][CH];  // [tile - 1]: d_j e^{G at the tile's start - G_j}, j before it
+  float total[4];              // G_n (its own 16 bytes)
 };
 
+__device__ __forceinline__ bfrag bfrag_of(u32x2 lo, u32x2 hi) {
+  return bf16x8_from_u32x4(u32x4{lo[0], lo[1], hi[0], hi[1]});
+}
 // Eight entries of a row at k = kperm(g, 0..7), two 8-byte reads.
 __device__ __forceinline__ bfrag frag_kperm(const __bf16* row, int g) {
   const u32x2 lo = *reinterpret_cast<const u32x2*>(row + 4 * g);
   const u32x2 hi = *reinterpret_cast<const u32x2*>(row + 16 + 4 * g);
-  return bf16x8_from_u32x4(u32x4{lo[0], lo[1], hi[0], hi[1]});
+  return bfrag_of(lo, hi);
 }
 // Column col0 + m of a row-major tile, rows 32 s + kperm(g, 0..7).
 __device__ __forceinline__ bfrag frag_col(const __bf16* tile, int ld, int col0, int s, int g, int m) {
@@ -249,15 +251,19 @@ struct Stage {
       r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(q, at + i * ROWS * ldb, 0, 0));
   }
   // as NP tiles of bf16 parts, `plane` entries apart
-  template <int NP>
+  template <int NP, bool WIDE>
   __device__ __forceinline__ void store(__bf16* to, int plane, int ld) const {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       const int p = i * kThreads + threadIdx.x, row = p / PER_ROW, c = p % PER_ROW * V;
       if constexpr (NP == 1) {
-        u32x2* const q = reinterpret_cast<u32x2*>(to + row * ld + c);
-        q[0] = u32x2{r[i][0], r[i][1]};
-        q[1] = u32x2{r[i][2], r[i][3]};
+        if constexpr (WIDE) {
+          *reinterpret_cast<u32x4*>(to + row * ld + c) = r[i];
+        } else {  // rows start on 8 bytes
+          u32x2* const q = reinterpret_cast<u32x2*>(to + row * ld + c);
+          q[0] = u32x2{r[i][0], r[i][1]};
+          q[1] = u32x2{r[i][2], r[i][3]};
+        }
       } else {
         const f32x4 v = __builtin_bit_cast(f32x4, r[i]);
         bf16x4 part[NP];
@@ -276,10 +282,21 @@ struct Stage {
   }
 };
 
-// The tiles of the lower triangle of CH / 16 x CH / 16 tiles, row by row.
-__device__ __forceinline__ void triangle(int i, int& tt, int& jt) {
-  tt = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3;
-  jt = i - tt * (tt + 1) / 2;
+// The tiles of the lower triangle of CH / 16 x CH / 16 tiles, dealt to the waves so that most of a
+// wave's tiles are of one row: three in rows 3 and 2, (1, 0), (1, 1) and (3, 3), (0, 0); of 32
+// tokens (0, 0), (1, 0) and (1, 1).
+template <int NT>
+__device__ __forceinline__ bool deal(int wave, int i, int& tt, int& jt) {
+  if constexpr (NT == 4) {
+    tt = 3 - wave;
+    jt = i;
+    if (wave == 2 && i == 2) tt = jt = 3;
+    return wave < 3 || i == 0;
+  } else {
+    tt = wave > 0;
+    jt = wave > 1;
+    return wave < 3;
+  }
 }
 
 // What a workgroup does with its segment: a whole request, outputs and state; the state of a
@@ -289,9 +306,10 @@ enum Mode { kWhole, kState, kOutput };
 template <typename T, int DK, int CH>
 struct Dims {
   static constexpr int NP = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of an input, scores and S in S C
-  // LDS rows. 8-byte reads down 16 rows take 4.5 cycles where the stride is 2 mod 4 words (70
-  // here), 8 or 16 elsewhere, transposed reads 6.4 there (measured, a wave's read).
-  static constexpr int LDC = DK + 12, LDB = DK + 12, LDX = kColsBlock + 12, LDP = CH + 8;
+  // LDS rows. C is read in 8-byte pieces down 16 rows: 4.5 cycles for a wave's read where the
+  // stride is 2 mod 4 words, 8 or 16 elsewhere. B and x are read transposed and in 16-byte pieces:
+  // no conflicts and 4.9 cycles where it is 8 mod 16 words, 8 elsewhere (measured).
+  static constexpr int LDC = DK + 12, LDB = DK + 16, LDX = kColsBlock + 16, LDP = CH + 8;
   static constexpr int TileC = CH * LDC, TileB = CH * LDB, TileX = CH * LDX, TileP = CH * LDP;
   using R = typename std::conditional<sizeof(T) == 4, double, float>::type;
   using G = Gates<CH, R>;
@@ -314,7 +332,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
   constexpr int NU = F32 ? 3 : MODE == kOutput ? 1 : 2;
   constexpr int NT = CH / 16, NK = CH / 32;      // token tiles, k steps over tokens
   constexpr int NS = DK / 16, NKS = DK / 32;     // state tiles, k steps over state entries
-  constexpr int NTRI = NT * (NT + 1) / 2, TRI = (NTRI + kWaves - 1) / kWaves;
+  constexpr int TRI = NT == 4 ? 3 : 1;           // tiles of scores for a wave at most
   constexpr int LDC = D::LDC, LDB = D::LDB, LDX = D::LDX, LDP = D::LDP;
   constexpr int kTileC = D::TileC, kTileB = D::TileB, kTileX = D::TileX, kTileP = D::TileP;
   __bf16* const s_b = reinterpret_cast<__bf16*>(lds);
@@ -400,9 +418,9 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
   for (int64_t t0 = sg.t0; t0 < sg.t1; t0 += CH, ++chunk) {
     if (t0 > sg.t0) __syncthreads();  // the chunk before has been read
     const int rows = sg.t1 - t0 < CH ? (int)(sg.t1 - t0) : CH;
-    qb.template store<NP>(s_b, kTileB, LDB);
-    if constexpr (OUT) qc.template store<NP>(s_c, kTileC, LDC);
-    qx.template store<NP>(s_x, kTileX, LDX);
+    qb.template store<NP, true>(s_b, kTileB, LDB);
+    if constexpr (OUT) qc.template store<NP, false>(s_c, kTileC, LDC);
+    qx.template store<NP, true>(s_x, kTileX, LDX);
     if (chunk % batch == 0) {
       // a gate set, a lane per token; rows past the end have no step and no decay
       G& gt = gate_set(gh, chunk + gc);
@@ -430,17 +448,17 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
           gt.row[lane] = exp2_((float)local);
 #pragma unroll
           for (int k = 1; k < NT; ++k)
-            gt.col[k][lane] = lane < 16 * k ? step * exp2_((float)(at[k] - Gp)) : 0.f;
+            gt.col[k - 1][lane] = lane < 16 * k ? step * exp2_((float)(at[k] - Gp)) : 0.f;
         }
         gt.w[lane] = step * exp2_(row_behind(gl) + after);
       }
-      if (lane == 0) gt.col[0][0] = (float)at[NT];
+      if (lane == 0) gt.total[0] = (float)at[NT];
       fetch_dt(t0 + batch * CH);
     }
     __syncthreads();
     if (t0 + CH < sg.t1) fetch(t0 + CH);
     const G& gt = gate_set(nh == 2 ? kColsWave * wv / a.dv : 0, chunk);
-    gsum += gt.total();
+    gsum += gt.total[0];
 
     bfrag xf[NP][2][NK];  // x, column p0 + 16 pt + r, tokens 32 k + kperm
 #pragma unroll
@@ -455,25 +473,27 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
       // scores^T, j x t: each wave some of the tiles, decayed for each of the workgroup's heads
 #pragma unroll
       for (int i = 0; i < TRI; ++i) {
-        const int n = wv + i * kWaves;
-        if (n >= NTRI) continue;
         int tt, jt;
-        triangle(n, tt, jt);
+        if (!deal<NT>(wv, i, tt, jt)) break;
         acc4 sc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < NKS; ++k)
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            const bfrag c = frag_kperm(s_c + p * kTileC + (16 * tt + r) * LDC + 32 * k, g);
+            const u32x2* const cp =
+                reinterpret_cast<const u32x2*>(s_c + p * kTileC + (16 * tt + r) * LDC + 32 * k + 8 * g);
+            const bfrag c = bfrag_of(cp[0], cp[1]);
 #pragma unroll
             for (int q = 0; q + p < NP; ++q)
-              sc = mma_bf16(frag_kperm(s_b + q * kTileB + (16 * jt + r) * LDB + 32 * k, g), c, sc);
+              sc = mma_bf16(*reinterpret_cast<const bfrag*>(s_b + q * kTileB + (16 * jt + r) * LDB +
+                                                            32 * k + 8 * g),
+                            c, sc);
           }
         for (int hh = 0; hh < nh; ++hh) {
           const G& gs = gate_set(hh, chunk);
           float v[4];
           if (jt < tt) {
-            const acc4 c = *reinterpret_cast<const acc4*>(&gs.col[tt][16 * jt + 4 * g]);
+            const acc4 c = *reinterpret_cast<const acc4*>(&gs.col[tt - 1][16 * jt + 4 * g]);
             const float row = gs.row[16 * tt + r];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = sc[e] * (c[e] * row);
@@ -588,7 +608,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 
     // S^T <- e^{G_n} S^T + B^T (w x)
     if (MODE == kOutput && t0 + CH >= sg.t1) break;  // nobody reads this state
-    const float eGn = exp2_(gt.total());
+    const float eGn = exp2_(gt.total[0]);
     bfrag xw[NU][2][NK];
 #pragma unroll
     for (int k = 0; k < NK; ++k)
