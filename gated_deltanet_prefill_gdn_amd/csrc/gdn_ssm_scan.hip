@@ -358,6 +358,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
   // gc after the batch's first.
   const int hv0 = h * a.rep + col0 / a.dv, nh = (ncols + a.dv - 1) / a.dv;
   const int batch = nh == 2 ? 2 : 4, gh = nh == 2 ? wv >> 1 : 0, gc = nh == 2 ? wv & 1 : wv;
+  const int hw = nh == 2 ? kColsWave * wv / a.dv : 0;
   auto gate_set = [&](int head, int chunk) -> G& {
     return s_g[nh == 2 ? 2 * head + (chunk & 1) : chunk & 3];
   };
@@ -386,7 +387,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 
   const float decay = -expf(a.A_log[hv0 + gh]) * kLog2e, dtb = a.dt_bias[hv0 + gh];
   const float dskip = a.D ? a.D[hv] : 0.f;
-  float gsum = 0.f;  // of g over the segment
+  float behind[kHeads] = {};  // a piece's state: sum of g over the chunks walked, of each head
 
   Stage<T, CH, DK> qb, qc;
   Stage<T, CH, kColsBlock> qx;
@@ -397,26 +398,32 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
     if constexpr (OUT) qc.load(gC + t * ldb, ldb, rows, DK);
     qx.load(gx + t * ldx, ldx, rows, ncols);
   };
-  auto fetch_dt = [&](int64_t t) {  // of this wave's set in the batch of chunks from t on
-    const int64_t left = sg.t1 - (t + gc * CH);
+  // The chunks in the order of the walk: outputs from the front. A piece's state alone is summed
+  // from its end, where the weights of its chunks are known, and the walk stops at chunks that
+  // have none.
+  const int chunks = (int)((sg.t1 - sg.t0 + CH - 1) / CH);
+  auto place = [&](int n) { return sg.t0 + (int64_t)(OUT ? n : chunks - 1 - n) * CH; };
+  auto fetch_dt = [&](int n) {  // of this wave's set in the batch of chunks from the n-th on
     qdt = 0.f;
-    if (left > 0)
+    if (n + gc < chunks) {
+      const int64_t t = place(n + gc), left = sg.t1 - t;
       qdt = __builtin_bit_cast(
           float, __builtin_amdgcn_raw_buffer_load_b32(
-                     chunk_rows(a.dt + (t + gc * CH) * a.HV + hv0 + gh, (int64_t)a.HV * 4,
+                     chunk_rows(a.dt + t * a.HV + hv0 + gh, (int64_t)a.HV * 4,
                                 left < CH ? (int)left : CH, 4),
                      lane * a.HV * 4, 0, 0));
+    }
   };
-  fetch(sg.t0);
-  fetch_dt(sg.t0);
+  fetch(place(0));
+  fetch_dt(0);
   if constexpr (OUT) {  // scores above the diagonal stay zero
     for (int i = tid; i < kHeads * NP * kTileP / 8; i += kThreads)
       reinterpret_cast<u32x4*>(s_p)[i] = u32x4{0, 0, 0, 0};
   }
 
-  int chunk = 0;
-  for (int64_t t0 = sg.t0; t0 < sg.t1; t0 += CH, ++chunk) {
-    if (t0 > sg.t0) __syncthreads();  // the chunk before has been read
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    const int64_t t0 = place(chunk);
+    if (chunk > 0) __syncthreads();  // the chunk before has been read
     const int rows = sg.t1 - t0 < CH ? (int)(sg.t1 - t0) : CH;
     qb.template store<NP, true>(s_b, kTileB, LDB);
     if constexpr (OUT) qc.template store<NP, false>(s_c, kTileC, LDC);
@@ -424,7 +431,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
     if (chunk % batch == 0) {
       // a gate set, a lane per token; rows past the end have no step and no decay
       G& gt = gate_set(gh, chunk + gc);
-      const bool in = lane < CH && t0 + gc * CH + lane < sg.t1;
+      const bool in = lane < CH && chunk + gc < chunks && place(chunk + gc) + lane < sg.t1;
       const float step = in ? softplusf(qdt + dtb) : 0.f;
       const float gl = in ? decay * step : 0.f;
       const R local = row_prefix((R)gl);
@@ -453,12 +460,11 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
         gt.w[lane] = step * exp2_(row_behind(gl) + after);
       }
       if (lane == 0) gt.total[0] = (float)at[NT];
-      fetch_dt(t0 + batch * CH);
+      fetch_dt(chunk + batch);
     }
     __syncthreads();
-    if (t0 + CH < sg.t1) fetch(t0 + CH);
-    const G& gt = gate_set(nh == 2 ? kColsWave * wv / a.dv : 0, chunk);
-    gsum += gt.total[0];
+    if (chunk + 1 < chunks) fetch(place(chunk + 1));
+    const G& gt = gate_set(hw, chunk);
 
     bfrag xf[NP][2][NK];  // x, column p0 + 16 pt + r, tokens 32 k + kperm
 #pragma unroll
@@ -535,7 +541,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
       __syncthreads();
       // Y^T, two token tiles at a time: columns 16 pt + 4 g .. + 3 of token 16 t + r
       const rsrc_t qo = chunk_rows(gout + t0 * ldx, ldx * (int)sizeof(T), rows, kColsWave * (int)sizeof(T));
-      const __bf16* const ph = s_p + (nh == 2 ? kColsWave * wv / a.dv : 0) * NP * kTileP;
+      const __bf16* const ph = s_p + hw * NP * kTileP;
 #pragma unroll 1
       for (int tp = 0; tp < NK; ++tp) {
         acc4 yc[2][2], yp[2][2];  // of S C (without its decay), of scores times x
@@ -607,14 +613,17 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
     }
 
     // S^T <- e^{G_n} S^T + B^T (w x)
-    if (MODE == kOutput && t0 + CH >= sg.t1) break;  // nobody reads this state
-    const float eGn = exp2_(gt.total[0]);
+    if (MODE == kOutput && chunk + 1 == chunks) break;  // nobody reads this state
+    // outputs: the state before decays over the chunk; a piece's state: the chunk's part decays
+    // over those behind it
+    const float eGn = OUT ? exp2_(gt.total[0]) : exp2_(behind[hw]);
     bfrag xw[NU][2][NK];
 #pragma unroll
     for (int k = 0; k < NK; ++k)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float w = gt.w[32 * k + kperm(g, e)];
+        float w = gt.w[32 * k + kperm(g, e)];
+        if constexpr (!OUT) w *= eGn;
 #pragma unroll
         for (int pt = 0; pt < 2; ++pt) {
           float v = 0.f;
@@ -629,7 +638,8 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
 #pragma unroll
-      for (int pt = 0; pt < 2; ++pt) st[s][pt] *= eGn;
+      for (int pt = 0; pt < 2; ++pt)
+        if constexpr (OUT) st[s][pt] *= eGn;
 #pragma unroll
       for (int k = 0; k < NK; ++k)
 #pragma unroll
@@ -640,6 +650,16 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 #pragma unroll
             for (int q = 0; q + p < NU; ++q) st[s][pt] = mma_bf16(b, xw[q][pt][k], st[s][pt]);
         }
+    }
+    if constexpr (!OUT) {
+      bool more = false;
+#pragma unroll
+      for (int hh = 0; hh < kHeads; ++hh)
+        if (hh < nh) {
+          behind[hh] += gate_set(hh, chunk).total[0];
+          more = more || !(exp2_(behind[hh]) == 0.f);
+        }
+      if (!more) break;  // every earlier weight is zero in fp32, and so is the piece's decay
     }
   }
 
@@ -652,7 +672,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 #pragma unroll
     for (int pt = 0; pt < 2; ++pt)
       *reinterpret_cast<acc4*>(to + 16 * pt * DK + 16 * s) = st[s][pt];
-  if (MODE == kState && p0 == 0 && lane == 0) a.seg_decay[(int64_t)sg.ws * a.HV + hv] = gsum;
+  if (MODE == kState && p0 == 0 && lane == 0) a.seg_decay[(int64_t)sg.ws * a.HV + hv] = behind[hw];
 }
 
 // The first launch (OUTPUT false): whole requests, and the states of cut ones' pieces. The last:
@@ -660,8 +680,13 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 template <typename T, int DK, int CH, bool OUTPUT>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DK < 256 ? 2 : 1) void ssm_scan_kernel(ScanArgs a) {
   __shared__ __align__(16) char lds[Dims<T, DK, CH>::Bytes];
-  const int per_seg = a.H * a.blocks_per_group;
-  const int seg = blockIdx.x / per_seg, in_seg = blockIdx.x % per_seg;
+  // Workgroups are dealt to the eight XCDs in turn: the column blocks of a (segment, group) go to
+  // one of them, one after the other, and find B and C in its L2. The XCD of a group changes from
+  // segment to segment, since groups differ in how far a piece's state reaches back.
+  const int turn = blockIdx.x / 8, row = turn / a.blocks_per_group;
+  const int unit = row * 8 + (blockIdx.x + 3 * row + row / 8) % 8;
+  const int seg = unit / a.H, in_seg = unit % a.H * a.blocks_per_group + turn % a.blocks_per_group;
+  if (a.lseg == 0 && seg >= a.nreq) return;  // units are a multiple of eight
   Segment sg;
   if (!find_segment(a, seg, sg)) return;
   if constexpr (OUTPUT) {
@@ -731,7 +756,8 @@ ScanLayout scan_layout(const SsmShape& s) {
 
 int64_t scan_blocks(const SsmShape& s) {
   const int lseg = segment_tokens(s);
-  return (s.B + (lseg ? s.N / lseg : 0)) * s.H * cdiv((int64_t)(s.HV / s.H) * s.dv, kColsBlock);
+  return cdiv((s.B + (lseg ? s.N / lseg : 0)) * s.H, 8) * 8 *
+         cdiv((int64_t)(s.HV / s.H) * s.dv, kColsBlock);
 }
 
 template <typename T, int DK, int CH>
