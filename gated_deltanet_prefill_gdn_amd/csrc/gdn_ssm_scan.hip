@@ -14,11 +14,11 @@
 // of one column, which is also what the next products want as an operand, so the state and the
 // scores never move between lanes.
 //
-// Requests longer than a segment are cut: a first launch forms each segment's state from zero (and
-// takes the requests that are not cut from start to end), a second joins the segments' states in
-// order into their start states and the final one, and a third forms the outputs of all segments
-// of cut requests side by side. Only the scalar decay per head lies between two segments, so the
-// join is one multiply-add per state entry and segment.
+// Requests longer than a segment are cut into equal pieces: a first launch forms each piece's
+// state from zero, a second joins the pieces' states in order into their start states and the
+// final one, and a third forms the outputs of all pieces side by side, and takes the requests that
+// are not cut from start to end. Only the scalar decay per head lies between two pieces, so the
+// join is one multiply-add per state entry and piece.
 //
 // Precision: bf16 inputs enter the products as they are. The decayed x of the state's update are
 // pairs of bf16 (hi + lo, at most 2^-17 off), since states are fp32 results; the decayed scores
@@ -62,9 +62,18 @@ struct ScanArgs {
   int max_cut;        // places in seg_state
 };
 
-// Segments of a request of L tokens (an empty request counts one, which has nothing to do).
-__device__ __forceinline__ int segments_of(int64_t L, int lseg) {
-  return lseg == 0 || L <= lseg ? 1 : (int)((L + lseg - 1) / lseg);
+// Pieces of a request of L tokens, and the tokens of one (a multiple of 64; the last piece may be
+// shorter): as equal as they come, at most lseg. An empty request counts one piece, which has
+// nothing to do.
+__device__ __forceinline__ int pieces_of(int64_t L64, int lseg, int& len) {
+  const int L = (int)L64;  // the call has less than 2^31 tokens
+  if (lseg == 0 || L64 <= lseg) {
+    len = L > 0 ? L : 0;
+    return 1;
+  }
+  const int n = (L + lseg - 1) / lseg;
+  len = ((L + n - 1) / n + 63) / 64 * 64;
+  return (L + len - 1) / len;
 }
 
 __device__ __forceinline__ int64_t begin_of(const ScanArgs& a, int64_t b) {
@@ -94,17 +103,20 @@ __device__ __forceinline__ int wave_inclusive(int v) {
 // Segment number `seg` of the call, by a scan over the requests, 64 at a time in every wave.
 __device__ __forceinline__ bool find_segment(const ScanArgs& a, int seg, Segment& s) {
   const int lane = threadIdx.x & 63;
+  int len;
   if (a.lseg == 0) {
     s.req = seg;
     s.index = 0;
     s.count = 1;
     s.ws = 0;
+    len = 0;
   } else {
     int before = 0, before_cut = 0;
     bool found = false;
     for (int64_t base = 0; base < a.nreq; base += 64) {
       const int64_t b = base + lane;
-      const int n = b < a.nreq ? segments_of(end_of(a, b) - begin_of(a, b), a.lseg) : 0;
+      int mine = 0;
+      const int n = b < a.nreq ? pieces_of(end_of(a, b) - begin_of(a, b), a.lseg, mine) : 0;
       const int inc = wave_inclusive(n), cut = wave_inclusive(n > 1 ? n : 0);
       const uint64_t over = __ballot(before + inc > seg);
       if (over) {
@@ -113,6 +125,7 @@ __device__ __forceinline__ bool find_segment(const ScanArgs& a, int seg, Segment
         s.index = seg - before - (__builtin_amdgcn_readlane(inc, k) - s.count);
         s.ws = before_cut + __builtin_amdgcn_readlane(cut, k) - s.count + s.index;
         s.req = base + k;
+        len = __builtin_amdgcn_readlane(mine, k);
         found = true;
         break;
       }
@@ -122,8 +135,8 @@ __device__ __forceinline__ bool find_segment(const ScanArgs& a, int seg, Segment
     if (!found) return false;
   }
   const int64_t begin = begin_of(a, s.req), end = end_of(a, s.req);
-  s.t0 = begin + (int64_t)s.index * a.lseg;
-  s.t1 = s.index + 1 < s.count ? s.t0 + a.lseg : end;
+  s.t0 = begin + (int64_t)s.index * len;
+  s.t1 = s.index + 1 < s.count ? s.t0 + len : end;
   const int64_t slot = a.idx[s.req];
   if (s.count > 1 && s.ws >= a.max_cut) return false;  // cu_seqlens breaks its precondition
   return s.t0 < s.t1 && slot >= 0 && slot < a.npool;
@@ -526,9 +539,9 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
                                        32 * (jt / 2) + 8 * g + 4 * (jt % 2)) = part[p];
         }
       }
-      bfrag sb[NP][2][NKS];  // S^T as the operand of S C
-#pragma unroll
-      for (int k = 0; k < NKS; ++k)
+      // S^T as the operand of S C: formed once for the chunk's token tiles, or, where there are
+      // but two of them, in their loop
+      auto state_operand = [&](int k, bfrag (&sb)[NP][2]) {
 #pragma unroll
         for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
@@ -536,8 +549,14 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
             __bf16 part[NP];
             split<NP>(st[2 * k + e / 4][pt][e % 4], part);
 #pragma unroll
-            for (int p = 0; p < NP; ++p) sb[p][pt][k][e] = part[p];
+            for (int p = 0; p < NP; ++p) sb[p][pt][e] = part[p];
           }
+      };
+      bfrag sbs[NK > 1 ? NKS : 1][NP][2];
+      if constexpr (NK > 1) {
+#pragma unroll
+        for (int k = 0; k < NKS; ++k) state_operand(k, sbs[k]);
+      }
       __syncthreads();
       // Y^T, two token tiles at a time: columns 16 pt + 4 g .. + 3 of token 16 t + r
       const rsrc_t qo = chunk_rows(gout + t0 * ldx, ldx * (int)sizeof(T), rows, kColsWave * (int)sizeof(T));
@@ -550,7 +569,9 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 #pragma unroll
           for (int pt = 0; pt < 2; ++pt) yc[u][pt] = yp[u][pt] = acc4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < NKS; ++k)
+        for (int k = 0; k < NKS; ++k) {
+          bfrag(&sb)[NP][2] = sbs[NK > 1 ? k : 0];
+          if constexpr (NK == 1) state_operand(k, sb);
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -560,8 +581,9 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 #pragma unroll
               for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
-                for (int q = 0; q + p < NP; ++q) yc[u][pt] = mma_bf16(sb[q][pt][k], c, yc[u][pt]);
+                for (int q = 0; q + p < NP; ++q) yc[u][pt] = mma_bf16(sb[q][pt], c, yc[u][pt]);
             }
+        }
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
           if (k > tp) break;
@@ -675,11 +697,10 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
   if (MODE == kState && p0 == 0 && lane == 0) a.seg_decay[(int64_t)sg.ws * a.HV + hv] = behind[hw];
 }
 
-// The first launch (OUTPUT false): whole requests, and the states of cut ones' pieces. The last:
-// the outputs of cut requests.
+// The pieces' states (OUTPUT false); the outputs of pieces, and whole requests.
 template <typename T, int DK, int CH, bool OUTPUT>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DK < 256 ? 2 : 1) void ssm_scan_kernel(ScanArgs a) {
-  __shared__ __align__(16) char lds[Dims<T, DK, CH>::Bytes];
+  __shared__ __align__(16) char lds[OUTPUT ? Dims<T, DK, CH>::Bytes : Dims<T, DK, CH>::AtC];
   // Workgroups are dealt to the eight XCDs in turn: the column blocks of a (segment, group) go to
   // one of them, one after the other, and find B and C in its L2. The XCD of a group changes from
   // segment to segment, since groups differ in how far a piece's state reaches back.
@@ -690,11 +711,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DK < 256 ? 2 : 1) void 
   Segment sg;
   if (!find_segment(a, seg, sg)) return;
   if constexpr (OUTPUT) {
-    if (sg.count > 1) scan_segment<T, DK, CH, kOutput>(a, sg, in_seg, lds);
+    if (sg.count > 1)
+      scan_segment<T, DK, CH, kOutput>(a, sg, in_seg, lds);
+    else
+      scan_segment<T, DK, CH, kWhole>(a, sg, in_seg, lds);
   } else if (sg.count > 1) {
     scan_segment<T, DK, CH, kState>(a, sg, in_seg, lds);
-  } else {
-    scan_segment<T, DK, CH, kWhole>(a, sg, in_seg, lds);
   }
 }
 
@@ -705,12 +727,13 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(ScanArgs a, int plane, in
   const int64_t req = pair / a.HV;
   const int hv = (int)(pair - req * a.HV);
   const int64_t slot = a.idx[req];
-  const int n = segments_of(end_of(a, req) - begin_of(a, req), a.lseg);
+  int len;
+  const int n = pieces_of(end_of(a, req) - begin_of(a, req), a.lseg, len);
   if (n <= 1 || slot < 0 || slot >= a.npool) return;
   int first = 0;  // place of the request's first segment
   for (int64_t base = 0; base < req; base += 64) {
     const int64_t b = base + (threadIdx.x & 63);
-    const int k = b < req ? segments_of(end_of(a, b) - begin_of(a, b), a.lseg) : 0;
+    const int k = b < req ? pieces_of(end_of(a, b) - begin_of(a, b), a.lseg, len) : 0;
     first += __builtin_amdgcn_readlane(wave_inclusive(k > 1 ? k : 0), 63);
   }
   const int e = (part * 256 + threadIdx.x) * 4;
@@ -728,15 +751,27 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(ScanArgs a, int plane, in
   *home = s;
 }
 
-// Tokens of a segment: enough segments to fill the device, each long enough that the state it
-// starts from and leaves is a small share of what it reads.
+// Tokens of a piece at most (0: no request is cut). A workgroup's time goes with its tokens, and
+// `slots` of them run at a time, so pieces are sized to fill k rounds of the device, k N / rounds
+// plus half a piece for every request, k = 1 .. 4: more rounds even out pieces of different
+// lengths, fewer spare the joins, which cost what kPieceTokens tokens do (a piece's state is
+// written, joined and read: 256 KB at dk = 128 for 128 columns, whose tokens take 0.75 KB).
+constexpr int kPieceTokens = 350;
 int segment_tokens(const SsmShape& s) {
   const int64_t blocks = cdiv((int64_t)(s.HV / s.H) * s.dv, kColsBlock) * s.H;
-  int64_t l = s.N * blocks / 1024;
-  l = (l + 63) / 64 * 64;
-  if (l < 512) l = 512;
-  if (l > 8192) l = 8192;
-  return s.N > l ? (int)l : 0;
+  const int64_t slots = s.dk < 256 ? 512 : 256;
+  int64_t best = 0, cost = INT64_MAX;
+  for (int k = 1; k <= 4; ++k) {
+    const int64_t pieces2 = 2 * k * slots / blocks - s.B;  // twice the pieces for N tokens
+    if (pieces2 <= 0) continue;
+    const int64_t l = cdiv(cdiv(2 * s.N, pieces2), 64) * 64;
+    if (k * (l + kPieceTokens) < cost) {
+      cost = k * (l + kPieceTokens);
+      best = l;
+    }
+  }
+  if (best < 512) best = best == 0 ? 0 : 512;
+  return s.N > best ? (int)best : 0;
 }
 
 // Segments of cut requests: each such request has more than lseg tokens, so at most twice
@@ -763,17 +798,16 @@ int64_t scan_blocks(const SsmShape& s) {
 template <typename T, int DK, int CH>
 hipError_t launch_scan(const SsmShape& s, const ScanArgs& a, hipStream_t st) {
   const unsigned blocks = (unsigned)scan_blocks(s);
-  hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, false>), dim3(blocks), dim3(kThreads), 0, st, a);
-  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (a.lseg) {
+    hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, false>), dim3(blocks), dim3(kThreads), 0, st, a);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int parts = s.dv * s.dk / 1024;
     hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)(s.B * s.HV * parts)), dim3(256), 0, st, a,
                        s.dv * s.dk, parts);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, true>), dim3(blocks), dim3(kThreads), 0, st, a);
-    return hipGetLastError();
   }
-  return hipSuccess;
+  hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, true>), dim3(blocks), dim3(kThreads), 0, st, a);
+  return hipGetLastError();
 }
 
 }  // namespace
