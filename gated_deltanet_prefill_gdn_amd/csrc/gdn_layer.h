@@ -148,7 +148,7 @@ struct SsmShape {
 };
 size_t ssm_workspace(const SsmShape& s);
 bool ssm_prefill_grids_fit(const SsmShape& s);
-bool ssm_decode_grid_fits(const SsmShape& s);
+bool ssm_token_grid_fits(const SsmShape& s);
 hipError_t launch_ssm_prefill(const SsmShape& s, const void* C, const void* B, const void* x,
                               const float* dt, const float* A_log, const float* dt_bias,
                               const float* D, float* state, const int64_t* idx,
@@ -157,6 +157,12 @@ hipError_t launch_ssm_decode(const SsmShape& s, const void* C, const void* B, co
                              const float* dt, const float* A_log, const float* dt_bias,
                              const float* D, float* state, const int64_t* idx, void* out,
                              hipStream_t st);
+
+// Requests of at most max_len tokens, token by token; the others are left alone.
+hipError_t launch_ssm_short(const SsmShape& s, const void* C, const void* B, const void* x,
+                            const float* dt, const float* A_log, const float* dt_bias,
+                            const float* D, float* state, const int64_t* idx, const int64_t* cu,
+                            void* out, int64_t max_len, hipStream_t st);
 
 }  // namespace layer
 }  // namespace gdn

@@ -217,7 +217,7 @@ gdn_status_t gdn_ssm_decode_fwd(const void* C, const void* B, const void* x, con
     return GDN_ERR_INVALID_ARG;
   for (const void* p : {C, B, x, (const void*)out, (const void*)state_pool})
     if (!aligned16(p)) return GDN_ERR_INVALID_ARG;
-  if (!ssm_decode_grid_fits(s)) return GDN_ERR_UNSUPPORTED;
+  if (!ssm_token_grid_fits(s)) return GDN_ERR_UNSUPPORTED;
   const hipError_t e = launch_ssm_decode(s, C, B, x, dt, A_log, dt_bias, D, state_pool,
                                          cache_indices, out, (hipStream_t)stream);
   return e == hipSuccess ? GDN_OK : GDN_ERR_HIP;

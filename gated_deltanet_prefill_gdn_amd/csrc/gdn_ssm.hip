@@ -1,4 +1,5 @@
-// One step of the selective state space scan.
+// Selective state space scan token by token: one step for single tokens, and short requests of a
+// prompt call, where a chunk of 64 rows would be mostly padding.
 //
 //   d = softplus(dt + dt_bias),  a = exp(-exp(A_log) d),  S <- a S + d x B^T,  out = S C + D x
 //
@@ -75,7 +76,7 @@ __global__ __launch_bounds__(kTokenThreads) void ssm_token_kernel(
     const float* __restrict__ dt_bias, const float* __restrict__ D,
     float* __restrict__ state_pool, const int64_t* __restrict__ idx,
     const int64_t* __restrict__ cu, T* __restrict__ out, int64_t N, int64_t pool, int H, int HV,
-    int DV, int nrb) {
+    int DV, int nrb, int64_t max_len) {
   constexpr int LPR = DK / 8, RPW = 64 / LPR, NR = kRowsPerThread<DK>, RWV = RPW * NR;
   const uint32_t pair = blockIdx.x / (uint32_t)nrb;
   const int rb = (int)(blockIdx.x - pair * (uint32_t)nrb);
@@ -87,7 +88,7 @@ __global__ __launch_bounds__(kTokenThreads) void ssm_token_kernel(
     t_end = cu[b + 1] < N ? cu[b + 1] : N;
   }
   const int64_t slot = idx[b];
-  if (t >= t_end || slot < 0 || slot >= pool) return;
+  if (t >= t_end || t_end - t > max_len || slot < 0 || slot >= pool) return;
   const int l = threadIdx.x & 63, gl = l % LPR;
   const int r0 = rb * kRowsPerBlock<DK> + (threadIdx.x >> 6) * RWV + l / LPR;
   float* const sp = state_pool + ((slot * HV + hv) * (int64_t)DV + r0) * DK + 4 * gl;
@@ -136,24 +137,24 @@ template <int DK, typename T>
 hipError_t launch_token(const SsmShape& s, const void* C, const void* B, const void* x,
                         const float* dt, const float* A_log, const float* dt_bias, const float* D,
                         float* state, const int64_t* idx, const int64_t* cu, void* out,
-                        hipStream_t st) {
+                        int64_t max_len, hipStream_t st) {
   hipLaunchKernelGGL((ssm_token_kernel<DK, T>), dim3((unsigned)token_blocks(s)),
                      dim3(kTokenThreads), 0, st, (const T*)C, (const T*)B, (const T*)x, dt, A_log,
                      dt_bias, D, state, idx, cu, (T*)out, s.N, s.pool, s.H, s.HV, s.dv,
-                     s.dv / kRowsPerBlock<DK>);
+                     s.dv / kRowsPerBlock<DK>, max_len);
   return hipGetLastError();
 }
 
 hipError_t launch_token_any(const SsmShape& s, const void* C, const void* B, const void* x,
                             const float* dt, const float* A_log, const float* dt_bias,
                             const float* D, float* state, const int64_t* idx, const int64_t* cu,
-                            void* out, hipStream_t st) {
+                            void* out, int64_t max_len, hipStream_t st) {
 #define GDN_SSM_CASE(DK)                                                                        \
   if (s.dk == DK)                                                                               \
     return s.bf16 ? launch_token<DK, __bf16>(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu, \
-                                             out, st)                                           \
+                                             out, max_len, st)                                  \
                   : launch_token<DK, float>(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu,  \
-                                            out, st);
+                                            out, max_len, st);
   GDN_SSM_CASE(64)
   GDN_SSM_CASE(128)
   GDN_SSM_CASE(256)
@@ -163,13 +164,20 @@ hipError_t launch_token_any(const SsmShape& s, const void* C, const void* B, con
 
 }  // namespace
 
-bool ssm_decode_grid_fits(const SsmShape& s) { return grid_ok(token_blocks(s), kTokenThreads); }
+bool ssm_token_grid_fits(const SsmShape& s) { return grid_ok(token_blocks(s), kTokenThreads); }
 
 hipError_t launch_ssm_decode(const SsmShape& s, const void* C, const void* B, const void* x,
                              const float* dt, const float* A_log, const float* dt_bias,
                              const float* D, float* state, const int64_t* idx, void* out,
                              hipStream_t st) {
-  return launch_token_any(s, C, B, x, dt, A_log, dt_bias, D, state, idx, nullptr, out, st);
+  return launch_token_any(s, C, B, x, dt, A_log, dt_bias, D, state, idx, nullptr, out, 1, st);
+}
+
+hipError_t launch_ssm_short(const SsmShape& s, const void* C, const void* B, const void* x,
+                            const float* dt, const float* A_log, const float* dt_bias,
+                            const float* D, float* state, const int64_t* idx, const int64_t* cu,
+                            void* out, int64_t max_len, hipStream_t st) {
+  return launch_token_any(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu, out, max_len, st);
 }
 
 }  // namespace layer

@@ -60,6 +60,7 @@ struct ScanArgs {
   int H, HV, dv, rep, blocks_per_group;
   int lseg;           // tokens of a segment (a multiple of 64), 0: nothing is cut
   int max_cut;        // places in seg_state
+  int short_len;      // requests of at most this many tokens are left to the token kernel
 };
 
 // Pieces of a request of L tokens, and the tokens of one (a multiple of 64; the last piece may be
@@ -139,7 +140,7 @@ __device__ __forceinline__ bool find_segment(const ScanArgs& a, int seg, Segment
   s.t1 = s.index + 1 < s.count ? s.t0 + len : end;
   const int64_t slot = a.idx[s.req];
   if (s.count > 1 && s.ws >= a.max_cut) return false;  // cu_seqlens breaks its precondition
-  return s.t0 < s.t1 && slot >= 0 && slot < a.npool;
+  return s.t0 < s.t1 && end - begin > a.short_len && slot >= 0 && slot < a.npool;
 }
 
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -722,7 +723,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DK < 256 ? 2 : 1) void 
 
 // Start states of a cut request's pieces, in place of the pieces' own states, and its final state.
 __global__ __launch_bounds__(256) void ssm_join_kernel(ScanArgs a, int plane, int parts) {
-  const int part = blockIdx.x % parts;
+  const int part = blockIdx.x % parts;  // every parts-th run of 1024 entries from this one on
   const int64_t pair = blockIdx.x / parts;
   const int64_t req = pair / a.HV;
   const int hv = (int)(pair - req * a.HV);
@@ -736,19 +737,20 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(ScanArgs a, int plane, in
     const int k = b < req ? pieces_of(end_of(a, b) - begin_of(a, b), a.lseg, len) : 0;
     first += __builtin_amdgcn_readlane(wave_inclusive(k > 1 ? k : 0), 63);
   }
-  const int e = (part * 256 + threadIdx.x) * 4;
-  if (first + n > a.max_cut) return;
-  f32x4* const home = reinterpret_cast<f32x4*>(a.pool + (slot * a.HV + hv) * (int64_t)plane + e);
-  f32x4 s = *home;
-  float* p = a.seg_state + ((int64_t)first * a.HV + hv) * plane + e;
-  const float* d = a.seg_decay + (int64_t)first * a.HV + hv;
+  if (first + n > a.max_cut) return;  // cu_seqlens breaks its precondition
+  const float* const d = a.seg_decay + (int64_t)first * a.HV + hv;
   const int64_t step = (int64_t)a.HV * plane;
-  for (int i = 0; i < n; ++i, p += step, d += a.HV) {
-    const f32x4 mine = *reinterpret_cast<const f32x4*>(p);
-    *reinterpret_cast<f32x4*>(p) = s;
-    s = s * exp2_(*d) + mine;
+  for (int e = (part * 256 + threadIdx.x) * 4; e < plane; e += parts * 1024) {
+    f32x4* const home = reinterpret_cast<f32x4*>(a.pool + (slot * a.HV + hv) * (int64_t)plane + e);
+    float* p = a.seg_state + ((int64_t)first * a.HV + hv) * plane + e;
+    f32x4 s = *home;
+    for (int i = 0; i < n; ++i, p += step) {
+      const f32x4 mine = *reinterpret_cast<const f32x4*>(p);
+      *reinterpret_cast<f32x4*>(p) = s;
+      s = s * exp2_(d[(int64_t)i * a.HV]) + mine;
+    }
+    *home = s;
   }
-  *home = s;
 }
 
 // Tokens of a piece at most (0: no request is cut). A workgroup's time goes with its tokens, and
@@ -772,6 +774,14 @@ int segment_tokens(const SsmShape& s) {
   }
   if (best < 512) best = best == 0 ? 0 : 512;
   return s.N > best ? (int)best : 0;
+}
+
+// Requests of at most this many tokens run token by token, where the mean length says that most
+// are and there are enough to fill the device (a call that splits pays a launch for the longer
+// ones too): 512 requests of 4 tokens, 32 heads of 128 x 128, take 382 us there and 483 in chunks,
+// of 8 tokens 559 and 491.
+int short_tokens(const SsmShape& s) {
+  return s.N <= 4 * s.B && s.B * s.HV * (s.dv / 64) >= 2048 ? 4 : 0;
 }
 
 // Segments of cut requests: each such request has more than lseg tokens, so at most twice
@@ -801,7 +811,9 @@ hipError_t launch_scan(const SsmShape& s, const ScanArgs& a, hipStream_t st) {
   if (a.lseg) {
     hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, false>), dim3(blocks), dim3(kThreads), 0, st, a);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    const int parts = s.dv * s.dk / 1024;
+    // enough workgroups to fill the device, few where many requests are likely not cut
+    int parts = s.dv * s.dk / 1024;
+    while (parts > 1 && s.B * s.HV * (parts / 2) >= 2048) parts /= 2;
     hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)(s.B * s.HV * parts)), dim3(256), 0, st, a,
                        s.dv * s.dk, parts);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
@@ -818,7 +830,8 @@ bool ssm_prefill_grids_fit(const SsmShape& s) {
   // the byte offsets inside a chunk's rows are 32-bit
   const int64_t row = (s.HV * (int64_t)s.dv > s.H * (int64_t)s.dk ? s.HV * (int64_t)s.dv
                                                                   : s.H * (int64_t)s.dk) * 4;
-  return row * 64 <= 0x7FFFFFFF && grid_ok(scan_blocks(s), kThreads) && grid_ok(s.B * s.HV * (s.dv * s.dk / 1024), 256);
+  return row * 64 <= 0x7FFFFFFF && grid_ok(scan_blocks(s), kThreads) &&
+         (!short_tokens(s) || ssm_token_grid_fits(s)) && grid_ok(s.B * s.HV * (s.dv * s.dk / 1024), 256);
 }
 
 hipError_t launch_ssm_prefill(const SsmShape& s, const void* C, const void* B, const void* x,
@@ -830,7 +843,12 @@ hipError_t launch_ssm_prefill(const SsmShape& s, const void* C, const void* B, c
   ScanArgs a{C, B, x, dt, A_log, dt_bias, D, state, idx, cu, out, (float*)(ws + L.state),
              (float*)(ws + L.decay), s.N, s.B, s.pool, s.H, s.HV, s.dv, s.HV / s.H,
              (int)cdiv((int64_t)(s.HV / s.H) * s.dv, kColsBlock), lseg,
-             (int)max_cut(s, lseg)};
+             (int)max_cut(s, lseg), short_tokens(s)};
+  if (a.short_len)
+    if (const hipError_t e = launch_ssm_short(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu,
+                                              out, a.short_len, st);
+        e != hipSuccess)
+      return e;
 #define GDN_SCAN_CASE(DK, CHB)                                        \
   if (s.dk == DK)                                                     \
     return s.bf16 ? launch_scan<__bf16, DK, CHB>(s, a, st) : launch_scan<float, DK, 32>(s, a, st);

@@ -181,6 +181,25 @@ def test_ssm_prompt_in_pieces(dtype):
     check(c, dtype, torch.cat(got), pool, f"ssm {dtype} in pieces")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ssm_short_requests_beside_a_long_one(dtype):
+    """Enough short requests that they run token by token, among them empty and longer ones."""
+    lengths = [1, 2, 3, 4, 0, 5, 1, 1] * 16 + [70]
+    c = make(16, lengths, 1, 16, 64, 64, dtype, dead=((9, -1),))
+    out, pool = call(c)
+    check(c, dtype, out, pool, f"ssm {dtype} short requests")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ssm_pieces_of_several_requests(dtype):
+    """Long requests cut into pieces between short and empty ones, decays slow enough that every
+    piece reaches the request's end, and fast enough that none does."""
+    for dt_mean, a_hi in ((-7.0, 1.5), (0.5, 16.0)):
+        c = make(17, [0, 2200, 31, 0, 1537, 600, 64], 2, 4, 64, 64, dtype, dt_mean=dt_mean, a_hi=a_hi)
+        out, pool = call(c)
+        check(c, dtype, out, pool, f"ssm {dtype} pieces, dt {dt_mean}")
+
+
 @pytest.mark.parametrize("seed", range(10))
 def test_ssm_random_shapes(seed):
     r = np.random.default_rng(100 + seed)
