@@ -166,35 +166,34 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(
     }
     const T* xp = x + t * x_stride + c;
     T* op = out + t * ld;
-    constexpr int U = 4;  // rows in flight
-    for (; t < run_end; t += U, xp += U * x_stride, op += U * ld) {
-      float cur[U][VEC];
-      const int n = run_end - t < U ? (int)(run_end - t) : U;
+    auto token = [&](const Raw<T, VEC>& cur, T* to) {
+      float y[VEC];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < n) load_vec<VEC>(xp + u * x_stride, cur[u]);
+      for (int e = 0; e < VEC; ++e) {
+        const float now = cur[e];
+        float a = b[e];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (u >= n) break;
-        float y[VEC];
+        for (int j = 0; j < W - 1; ++j) a = __builtin_fmaf(w[j][e], win[j][e], a);
+        a = __builtin_fmaf(w[W - 1][e], now, a);
+        y[e] = SILU ? a * sigmoidf(a) : a;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          float a = b[e];
-#pragma unroll
-          for (int j = 0; j < W - 1; ++j) a = __builtin_fmaf(w[j][e], win[j][e], a);
-          a = __builtin_fmaf(w[W - 1][e], cur[u][e], a);
-          y[e] = SILU ? a * sigmoidf(a) : a;
-        }
-        store_vec<VEC>(op + u * ld, y);
-#pragma unroll
-        for (int j = 0; j + 1 < W - 1; ++j)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) win[W - 2][e] = cur[u][e];
+        for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
+        win[W - 2][e] = now;
       }
+      store_vec<VEC>(to, y);
+    };
+    constexpr int U = 4;  // rows in flight
+    Raw<T, VEC> cur[U];
+    for (; t + U <= run_end; t += U, xp += U * x_stride, op += U * ld) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) cur[u].load(xp + u * x_stride);
+#pragma unroll
+      for (int u = 0; u < U; ++u) token(cur[u], op + u * ld);
     }
-    t = run_end;
+    for (; t < run_end; ++t, xp += x_stride, op += ld) {
+      cur[0].load(xp);
+      token(cur[0], op);
+    }
   }
 }
 
@@ -236,8 +235,11 @@ __global__ __launch_bounds__(kThreads) void conv_decode_kernel(
 
 // ---- gradients
 
-// Workgroup of the backward: kCols threads along the channels, kRuns runs of tokens.
-constexpr int kCols = 32, kRuns = kThreads / kCols;
+// Workgroup of the backward: kCols threads along the channels, kRuns runs of tokens. A thread
+// holds weights, their gradients, the window and the g of W tokens for each of its channels:
+// four channels leave room for four waves on a SIMD, eight (16 bytes of bf16) for one.
+constexpr int kVecBwd = 4;
+constexpr int kCols = 64, kRuns = kThreads / kCols;
 
 template <typename T, typename TG, int VEC, int W, bool SILU>
 __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(
@@ -461,6 +463,7 @@ int bwd_run(const ConvShape& s, int vec) {
 }
 
 int vec_of(const ConvShape& s) { return s.vec ? (s.bf16 ? 8 : 4) : 1; }
+int vec_bwd(const ConvShape& s) { return s.vec ? kVecBwd : 1; }
 
 template <typename T, int VEC, int W, bool SILU>
 hipError_t conv_fwd_t(const ConvShape& s, const void* x, const float* weight, const float* bias,
@@ -570,7 +573,7 @@ hipError_t conv_bwd_v(const ConvShape& s, const void* x, const float* weight, co
 }  // namespace
 
 bool conv_grids_fit(const ConvShape& s, bool backward) {
-  const int vec = vec_of(s);
+  const int vec = backward ? vec_bwd(s) : vec_of(s);
   const int64_t cols = cdiv(s.ch, (int64_t)vec * (backward ? kCols : kThreads));
   const int64_t x = backward ? cdiv(s.N, (int64_t)bwd_run(s, vec) * kRuns)
                              : cdiv(s.N, fwd_tile(s, vec));
@@ -596,7 +599,7 @@ size_t conv_bwd_workspace(const ConvShape& s) {
   size_t rows = 0;
   for (const bool vec : {false, true}) {
     t.vec = vec;
-    const size_t r = (size_t)cdiv(s.N, (int64_t)bwd_run(t, vec_of(t)) * kRuns);
+    const size_t r = (size_t)cdiv(s.N, (int64_t)bwd_run(t, vec_bwd(t)) * kRuns);
     rows = r > rows ? r : rows;
   }
   return align256(rows * (size_t)(s.W + 1) * (size_t)s.ch * sizeof(float));
@@ -614,10 +617,10 @@ hipError_t launch_conv_bwd(const ConvShape& s, const void* x, const float* weigh
                                 dbias, dstate0, ws, st)
   if (s.bf16) {
     if (s.dout_bf16) {
-      if (s.vec) GDN_CONV_BWD(__bf16, __bf16, 8);
+      if (s.vec) GDN_CONV_BWD(__bf16, __bf16, kVecBwd);
       GDN_CONV_BWD(__bf16, __bf16, 1);
     }
-    if (s.vec) GDN_CONV_BWD(__bf16, float, 8);
+    if (s.vec) GDN_CONV_BWD(__bf16, float, kVecBwd);
     GDN_CONV_BWD(__bf16, float, 1);
   }
   if (s.dout_bf16) {

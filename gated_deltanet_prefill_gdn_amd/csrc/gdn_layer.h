@@ -52,6 +52,24 @@ __device__ __forceinline__ void load_vec(const __bf16* p, float (&x)[VEC]) {
   }
 }
 
+// The same in the stored type: what a load leaves in registers until its use (half the registers
+// of fp32 for bf16).
+template <typename T, int VEC>
+struct Raw {
+  typedef T vec_t __attribute__((ext_vector_type(VEC)));
+  vec_t v;
+  __device__ __forceinline__ void load(const T* p) { v = *reinterpret_cast<const vec_t*>(p); }
+  __device__ __forceinline__ void zero() { v = (vec_t)(T)0.f; }
+  __device__ __forceinline__ float operator[](int e) const { return (float)v[e]; }
+};
+template <typename T>
+struct Raw<T, 1> {
+  T v;
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ void zero() { v = (T)0.f; }
+  __device__ __forceinline__ float operator[](int) const { return (float)v; }
+};
+
 // Rounded once to the stored type (round to nearest even, NaN stays NaN).
 template <int VEC>
 __device__ __forceinline__ void store_vec(float* p, const float (&x)[VEC]) {
@@ -71,6 +89,9 @@ __device__ __forceinline__ void store_vec(__bf16* p, const float (&x)[VEC]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = (__bf16)x[e];
     *reinterpret_cast<bf16x8*>(p) = v;
+  } else if constexpr (VEC == 4) {
+    *reinterpret_cast<bf16x4*>(p) =
+        bf16x4{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) p[i] = (__bf16)x[i];

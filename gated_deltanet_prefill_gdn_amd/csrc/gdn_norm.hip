@@ -283,27 +283,33 @@ __global__ __launch_bounds__(kBlock<TPR>) void norm_bwd_kernel(
   }
 }
 
-// dweight and dbias from the workgroups' partial rows [blocks][2][dim], added in order.
-__global__ __launch_bounds__(256) void norm_bwd_sum_kernel(const float* __restrict__ partial,
-                                                           int blocks, int dim,
-                                                           float* __restrict__ dweight,
-                                                           float* __restrict__ dbias) {
-  constexpr int C = 16, R = 256 / C;
-  __shared__ float s_red[R][C];
-  const int col = threadIdx.x % C, r = threadIdx.x / C;
-  const int c = (int)blockIdx.x * C + col;
+// dweight and dbias from the workgroups' partial rows [blocks][2][dim], added in a fixed order: a
+// thread's rows four at a time, then the threads of a column.
+constexpr int kSumCols = 16, kSumRows = 64;
+__global__ __launch_bounds__(kSumCols * kSumRows) void norm_bwd_sum_kernel(
+    const float* __restrict__ partial, int blocks, int dim, float* __restrict__ dweight,
+    float* __restrict__ dbias) {
+  __shared__ float s_red[kSumRows][kSumCols + 1];
+  const int col = threadIdx.x % kSumCols, r = threadIdx.x / kSumCols;
+  const int c = (int)blockIdx.x * kSumCols + col;
   float* const to = blockIdx.y ? dbias : dweight;
   if (!to) return;  // the whole workgroup
+  const float* const p = partial + (int64_t)blockIdx.y * dim + c;
   float v = 0.f;
-  if (c < dim)
-    for (int k = r; k < blocks; k += R) v += partial[((int64_t)k * 2 + blockIdx.y) * dim + c];
-  s_red[r][col] = v;
-  __syncthreads();
-  if (r == 0 && c < dim) {
+  if (c < dim) {
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = r; k < blocks; k += 4 * kSumRows)
 #pragma unroll
-    for (int i = 1; i < R; ++i) v += s_red[i][col];
-    to[c] = v;
+      for (int i = 0; i < 4; ++i)
+        if (k + i * kSumRows < blocks) a[i] += p[(int64_t)(k + i * kSumRows) * 2 * dim];
+    v = (a[0] + a[1]) + (a[2] + a[3]);
   }
+  s_red[r][col] = v;
+  for (int half = kSumRows / 2; half > 0; half /= 2) {
+    __syncthreads();
+    if (r < half) s_red[r][col] += s_red[r + half][col];
+  }
+  if (r == 0 && c < dim) to[c] = s_red[0][col];
 }
 
 // Rows handled at a time by one workgroup of the kernel that serves a row length.
@@ -448,8 +454,8 @@ hipError_t launch_norm_bwd(const NormShape& s, const void* x, const float* weigh
                 : bwd_v<float, 1>(s, p, x, weight, bias, z, dout, dx, dz, ws, st);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(norm_bwd_sum_kernel, dim3((unsigned)cdiv(s.dim, 16), 2), dim3(256), 0, st,
-                     ws, (int)blocks, s.dim, dweight, dbias);
+  hipLaunchKernelGGL(norm_bwd_sum_kernel, dim3((unsigned)cdiv(s.dim, kSumCols), 2),
+                     dim3(kSumCols * kSumRows), 0, st, ws, (int)blocks, s.dim, dweight, dbias);
   return hipGetLastError();
 }
 

@@ -8,16 +8,17 @@ computation runs in the library's HIP kernels.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
-from . import (GDN_DTYPE_BF16, GDN_DTYPE_F32, GDN_OK, GdnError, GdnProblem, _need, load_library,
-               make_problem)
+from . import (GDN_DTYPE_BF16, GDN_DTYPE_F32, GDN_OK, GdnError, GdnProblem, _need, load_library)
 
 GDN_CONV_SILU = 1
 GDN_NORM_RMS = 1
 GDN_NORM_GATE_FIRST = 2
 
+_Three = ctypes.c_int32 * 3
 _CODES = {torch.bfloat16: GDN_DTYPE_BF16, torch.float32: GDN_DTYPE_F32}
 _F32, _I64 = torch.float32, torch.int64
 
@@ -29,7 +30,7 @@ class GdnConvProblem(ctypes.Structure):
         ("pool_size", ctypes.c_int64),
         ("x_stride", ctypes.c_int64),
         ("dx_stride", ctypes.c_int64),
-        ("channels", ctypes.c_int32 * 3),
+        ("channels", _Three),
         ("width", ctypes.c_int32),
         ("dtype", ctypes.c_int32),
         ("dout_dtype", ctypes.c_int32),
@@ -54,36 +55,43 @@ class GdnNormProblem(ctypes.Structure):
 
 
 def _code(t, name):
-    try:
-        return _CODES[t.dtype]
-    except KeyError:
-        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}") from None
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return code
 
 
-def _shape(t, name, shape, dtype, device):
-    """t: a dense tensor of this shape, dtype and device."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    _need(t, name, dtype=dtype, device=device)
+def _shape(t, name, shape, dtype, like):
+    """t: a dense tensor of this shape and dtype on the device of `like`."""
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != like.get_device()
+            or not t.is_contiguous()):
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        _need(t, name, dtype=dtype, device=like.device)
 
 
-def _rows(t, name, inner, dtype, device):
-    """Token stride of t, whose tokens are dense rows of `inner` shape some stride apart."""
-    if t.dim() != 1 + len(inner) or t.shape[1:] != inner:
+def _rows(t, name, inner, like):
+    """Token stride of t, whose tokens are dense rows of `inner` shape some stride apart, of the
+    dtype and on the device of `like`."""
+    if t.shape[1:] != inner:
         raise ValueError(f"{name} must be [N, {', '.join(map(str, inner))}], got {list(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    size = 1
+    if t.dtype is not like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    size = math.prod(inner)
+    if t.is_contiguous():
+        return size
+    dense = 1
     for d, st in zip(reversed(inner), reversed(t.stride()[1:])):
-        if st != size and d != 1 and t.numel():
+        if st != dense and d != 1:
             raise ValueError(f"{name}: the entries of a token must be dense")
-        size *= d
-    n = t.shape[0]
-    if n > 1 and t.stride(0) < size:
+        dense *= d
+    if t.shape[0] <= 1:
+        return size
+    if t.stride(0) < size:
         raise ValueError(f"{name}: tokens overlap (stride {t.stride(0)} for rows of {size})")
-    return t.stride(0) if n > 1 else size
+    return t.stride(0)
 
 
 def _p(t):
@@ -95,14 +103,16 @@ def _call(what, device, stream, fn, *args):
     if device.type != "cuda":
         raise ValueError(f"{what} runs on a HIP device; tensors are on {device}")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        raw = torch._C._cuda_getCurrentRawStream(device.index)  # 1.7 us less than current_stream()
     elif stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    else:
+        raw = stream.cuda_stream
     if device.index == torch.cuda.current_device():
-        rc = fn(*args, stream.cuda_stream)
+        rc = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, stream.cuda_stream)
+            rc = fn(*args, raw)
     if rc != GDN_OK:
         raise GdnError(rc, what)
 
@@ -114,15 +124,20 @@ def _workspace(workspace, need, device):
     return workspace
 
 
-def _requests(cache_indices, cu_seqlens, device):
+def _index(t, name, like):
+    if (t.dtype is not _I64 or t.dim() != 1 or t.get_device() != like.get_device()
+            or not t.is_contiguous()):
+        _need(t, name, dtype=_I64, ndim=1, device=like.device)
+    return t.shape[0]
+
+
+def _requests(cache_indices, cu_seqlens, like):
     """B; cache_indices may be None (a convolution without a state pool)."""
-    if cache_indices is not None:
-        _need(cache_indices, "cache_indices", dtype=_I64, ndim=1, device=device)
+    n = None if cache_indices is None else _index(cache_indices, "cache_indices", like)
     if cu_seqlens is None:
-        return cache_indices.shape[0]
-    _need(cu_seqlens, "cu_seqlens", dtype=_I64, ndim=1, device=device)
-    b = cu_seqlens.shape[0] - 1
-    if b < 0 or (cache_indices is not None and cache_indices.shape[0] != b):
+        return n
+    b = _index(cu_seqlens, "cu_seqlens", like) - 1
+    if b < 0 or (n is not None and n != b):
         raise ValueError("cu_seqlens must have B + 1 entries")
     return b
 
@@ -132,14 +147,13 @@ def _requests(cache_indices, cu_seqlens, device):
 def conv_problem(x, width, dims, batch, pool_size=0, silu=True, dout_dtype=GDN_DTYPE_F32,
                  dx_stride=None) -> GdnConvProblem:
     """Descriptor of a convolution of x [N, sum(dims)] (see gdn_conv_problem_t)."""
-    dims = tuple(int(d) for d in dims)
     if not 1 <= len(dims) <= 3:
         raise ValueError("one to three outputs")
     ch = sum(dims)
-    stride = _rows(x, "x", (ch,), x.dtype, x.device)
+    stride = _rows(x, "x", (ch,), x)
     return GdnConvProblem(x.shape[0], batch, pool_size, stride,
                           ch if dx_stride is None else dx_stride,
-                          (ctypes.c_int32 * 3)(*(dims + (0, 0, 0))[:3]), width, _code(x, "x"),
+                          _Three(*dims), width, _code(x, "x"),
                           dout_dtype, GDN_CONV_SILU if silu else 0, 0)
 
 
@@ -154,28 +168,29 @@ def _conv_check(x, weight, bias, state_pool, cache_indices, cu_seqlens, dims, si
     if weight.dim() != 2 or weight.shape[0] != ch:
         raise ValueError(f"weight must be [{ch}, W], got {list(weight.shape)}")
     w = weight.shape[1]
-    _need(weight, "weight", dtype=_F32, device=dev)
+    _shape(weight, "weight", (ch, w), _F32, x)
     if bias is not None:
-        _shape(bias, "bias", (ch,), _F32, dev)
+        _shape(bias, "bias", (ch,), _F32, x)
     if state_pool is None and cache_indices is not None and cu_seqlens is None:
         raise ValueError("state_pool is required")
     if state_pool is not None:
         if cache_indices is None:
             raise ValueError("cache_indices are required with a state_pool")
-        _shape(state_pool, "state_pool", (state_pool.shape[0], w - 1, ch), x.dtype, dev)
-    batch = _requests(cache_indices if state_pool is not None else None, cu_seqlens, dev)
+        _shape(state_pool, "state_pool", (state_pool.shape[0], w - 1, ch), x.dtype, x)
+    batch = _requests(cache_indices if state_pool is not None else None, cu_seqlens, x)
     prob = conv_problem(x, w, dims, batch, 0 if state_pool is None else state_pool.shape[0], silu,
                         **kw)
     return dev, dims, prob
 
 
-def _conv_outs(outs, n, dims, dtype, dev):
+def _conv_outs(outs, x, dims):
+    n = x.shape[0]
     if outs is None:
-        return tuple(torch.empty((n, d), dtype=dtype, device=dev) for d in dims)
+        return tuple([x.new_empty((n, d)) for d in dims])
     if len(outs) != len(dims):
         raise ValueError(f"{len(dims)} outputs are wanted, got {len(outs)}")
     for i, (o, d) in enumerate(zip(outs, dims)):
-        _shape(o, f"outs[{i}]", (n, d), dtype, dev)
+        _shape(o, f"outs[{i}]", (n, d), x.dtype, x)
     return tuple(outs)
 
 
@@ -197,7 +212,7 @@ def gdn_conv_fwd(x, weight, bias, state_pool, cache_indices, cu_seqlens, dims=No
     outputs are not written."""
     dev, dims, prob = _conv_check(x, weight, bias, state_pool, cache_indices, cu_seqlens, dims,
                                   silu)
-    outs = _conv_outs(outs, x.shape[0], dims, x.dtype, dev)
+    outs = _conv_outs(outs, x, dims)
     _call("gdn_conv_fwd", dev, stream, load_library().gdn_conv_fwd, _p(x), _p(weight), _p(bias),
           _p(state_pool), _p(cache_indices), _p(cu_seqlens), *_three(outs), ctypes.byref(prob))
     return outs
@@ -207,7 +222,7 @@ def gdn_conv_decode_fwd(x, weight, bias, state_pool, cache_indices, dims=None, s
                         outs=None, stream=None):
     """gdn_conv_fwd for one new token per request: x [B, channels], row b with request b."""
     dev, dims, prob = _conv_check(x, weight, bias, state_pool, cache_indices, None, dims, silu)
-    outs = _conv_outs(outs, x.shape[0], dims, x.dtype, dev)
+    outs = _conv_outs(outs, x, dims)
     _call("gdn_conv_decode_fwd", dev, stream, load_library().gdn_conv_decode_fwd, _p(x),
           _p(weight), _p(bias), _p(state_pool), _p(cache_indices), *_three(outs),
           ctypes.byref(prob))
@@ -231,18 +246,18 @@ def gdn_conv_bwd(x, weight, bias, state_pool, cache_indices, cu_seqlens, douts, 
     dims = tuple(d.shape[1] for d in douts)
     n, dev = x.shape[0], x.device
     for i, d in enumerate(douts):
-        _shape(d, f"douts[{i}]", (n, dims[i]), douts[0].dtype, dev)
+        _shape(d, f"douts[{i}]", (n, dims[i]), douts[0].dtype, x)
     ch = x.shape[1] if x.dim() == 2 else 0
     if dx is None:
         dx = torch.empty((n, ch), dtype=x.dtype, device=dev)
     dev, dims, prob = _conv_check(x, weight, bias, state_pool, cache_indices, cu_seqlens, dims,
                                   silu, dout_dtype=_code(douts[0], "douts"),
-                                  dx_stride=_rows(dx, "dx", (ch,), x.dtype, dev))
+                                  dx_stride=_rows(dx, "dx", (ch,), x))
     if dx.shape[0] != n:
         raise ValueError("dx must have N rows")
     b, w = prob.batch, prob.width
     if dstate is not None:
-        _shape(dstate, "dstate", (b, w - 1, ch), _F32, dev)
+        _shape(dstate, "dstate", (b, w - 1, ch), _F32, x)
     g = {"dx": dx, "dweight": torch.empty((ch, w), dtype=_F32, device=dev)}
     if bias is not None:
         g["dbias"] = torch.empty((ch,), dtype=_F32, device=dev)
@@ -267,25 +282,26 @@ def _ssm_check(C, B, x, dt, A_log, dt_bias, D, state_pool, cache_indices, cu_seq
     if x.dim() != 3 or B.dim() != 3:
         raise ValueError("x must be [N, HV, dv] and B [N, H, dk]")
     n, hv, dv = x.shape
-    h, dk = B.shape[1:]
+    _, h, dk = B.shape
     code = _code(x, "x")
-    _need(x, "x")
-    _shape(B, "B", (n, h, dk), x.dtype, dev)
-    _shape(C, "C", (n, h, dk), x.dtype, dev)
-    _shape(dt, "dt", (n, hv), _F32, dev)
-    _shape(A_log, "A_log", (hv,), _F32, dev)
-    _shape(dt_bias, "dt_bias", (hv,), _F32, dev)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    _shape(B, "B", (n, h, dk), x.dtype, x)
+    _shape(C, "C", (n, h, dk), x.dtype, x)
+    _shape(dt, "dt", (n, hv), _F32, x)
+    _shape(A_log, "A_log", (hv,), _F32, x)
+    _shape(dt_bias, "dt_bias", (hv,), _F32, x)
     if D is not None:
-        _shape(D, "D", (hv,), _F32, dev)
-    _shape(state_pool, "state_pool", (state_pool.shape[0], hv, dv, dk), _F32, dev)
-    batch = _requests(cache_indices, cu_seqlens, dev)
+        _shape(D, "D", (hv,), _F32, x)
+    _shape(state_pool, "state_pool", (state_pool.shape[0], hv, dv, dk), _F32, x)
+    batch = _requests(cache_indices, cu_seqlens, x)
     if cu_seqlens is None and batch != n:
         raise ValueError("cache_indices must have one entry per row of x")
     if out is None:
-        out = torch.empty((n, hv, dv), dtype=x.dtype, device=dev)
+        out = x.new_empty((n, hv, dv))
     else:
-        _shape(out, "out", (n, hv, dv), x.dtype, dev)
-    return dev, out, make_problem(n, batch, h, hv, dk, dv, state_pool.shape[0], code)
+        _shape(out, "out", (n, hv, dv), x.dtype, x)
+    return dev, out, GdnProblem(n, batch, h, hv, dk, dv, state_pool.shape[0], code, 0)
 
 
 def gdn_ssm_prefill_fwd(C, B, x, dt, A_log, dt_bias, D, state_pool, cache_indices, cu_seqlens,
@@ -323,9 +339,9 @@ def gdn_ssm_decode_fwd(C, B, x, dt, A_log, dt_bias, D, state_pool, cache_indices
 def norm_problem(x, z=None, eps=1e-6, rms=True, gate_first=False, dz=None) -> GdnNormProblem:
     """Descriptor of a norm of x [N, heads, dim] (see gdn_norm_problem_t)."""
     inner = x.shape[1:]
-    xs = _rows(x, "x", inner, x.dtype, x.device)
-    zs = 0 if z is None else _rows(z, "z", inner, x.dtype, x.device)
-    dzs = zs if dz is None else _rows(dz, "dz", inner, x.dtype, x.device)
+    xs = _rows(x, "x", inner, x)
+    zs = 0 if z is None else _rows(z, "z", inner, x)
+    dzs = zs if dz is None else _rows(dz, "dz", inner, x)
     return GdnNormProblem(x.shape[0], xs, zs, dzs, inner[0], inner[1], _code(x, "x"),
                           (GDN_NORM_RMS if rms else 0) | (GDN_NORM_GATE_FIRST if gate_first else 0),
                           eps, 0)
@@ -336,9 +352,9 @@ def _norm_check(x, weight, bias, z, eps, rms, gate_first, dz=None):
     if x.dim() != 3:
         raise ValueError(f"x must be [N, heads, dim], got {list(x.shape)}")
     dim = x.shape[2]
-    _shape(weight, "weight", (dim,), _F32, dev)
+    _shape(weight, "weight", (dim,), _F32, x)
     if bias is not None:
-        _shape(bias, "bias", (dim,), _F32, dev)
+        _shape(bias, "bias", (dim,), _F32, x)
     for t, name in ((z, "z"), (dz, "dz")):
         if t is not None and t.shape != x.shape:
             raise ValueError(f"{name} must have x's shape {list(x.shape)}, got {list(t.shape)}")
@@ -356,9 +372,9 @@ def gdn_norm_fwd(x, weight, bias=None, z=None, eps: float = 1e-6, rms: bool = Tr
     None fp32, shared by the heads; 1 <= dim <= 16384."""
     dev, prob = _norm_check(x, weight, bias, z, eps, rms, gate_first)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = x.new_empty(x.shape)
     else:
-        _shape(out, "out", x.shape, x.dtype, dev)
+        _shape(out, "out", x.shape, x.dtype, x)
     _call("gdn_norm_fwd", dev, stream, load_library().gdn_norm_fwd, _p(x), _p(weight), _p(bias),
           _p(z), _p(out), ctypes.byref(prob))
     return out
@@ -377,7 +393,7 @@ def gdn_norm_bwd(x, weight, bias, z, dout, eps: float = 1e-6, rms: bool = True,
     elif z is None and dz is not None:
         raise ValueError("dz without a gate z")
     dev, prob = _norm_check(x, weight, bias, z, eps, rms, gate_first, dz)
-    _shape(dout, "dout", x.shape, x.dtype, dev)
+    _shape(dout, "dout", x.shape, x.dtype, x)
     g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
          "dweight": torch.empty(weight.shape, dtype=_F32, device=dev)}
     if z is not None:
