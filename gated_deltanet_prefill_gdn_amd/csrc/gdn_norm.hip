@@ -82,6 +82,37 @@ __device__ __forceinline__ void load_cols(const T* p, const int (&col)[NC], cons
   }
 }
 
+// The same as they are stored, for rows that wait in registers: with the backward's rows loaded as
+// they are and converted at their use its gated rows of 128 take 64 us instead of 94.
+template <typename T, int VEC, int NC>
+__device__ __forceinline__ void load_raw(const T* p, const int (&col)[NC], const bool (&in)[NC],
+                                         Raw<T, VEC> (&v)[NC]) {
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    if (in[i])
+      v[i].load(p + col[i]);
+    else
+      v[i].zero();
+  }
+}
+template <typename T, int VEC, int NC>
+__device__ __forceinline__ void unpack(const Raw<T, VEC> (&v)[NC], float (&x)[NC][VEC]) {
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[i][e] = v[i][e];
+}
+
+// Where a row group's row of a step of the loop is: token, head, and whether it exists.
+struct RowAt {
+  int64_t row, t, h;
+  bool live;
+  __device__ __forceinline__ RowAt(int64_t r, const NormArgs& a) : row(r), live(r < a.rows) {
+    t = live ? r / a.heads : 0;
+    h = live ? r - t * a.heads : 0;
+  }
+};
+
 // Workgroup threads: at least one row, 256 where rows are narrower.
 template <int TPR>
 constexpr int kBlock = TPR > 256 ? TPR : 256;
@@ -128,16 +159,14 @@ __global__ __launch_bounds__(kBlock<TPR>) void norm_fwd_kernel(
   const int64_t step = (int64_t)gridDim.x * RPB;
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += step) {
     // a wider row's threads leave the loop together; a narrow one's past the end do no harm
-    const int64_t row = r0 + rg;
-    const bool live = row < a.rows;
-    const int64_t t = live ? row / a.heads : 0, h = live ? row - t * a.heads : 0;
+    const RowAt at(r0 + rg, a);
     bool in[NC];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) in[i] = k.in[i] && live;
+    for (int i = 0; i < NC; ++i) in[i] = k.in[i] && at.live;
     float u[NC][VEC], g[NC][VEC];
-    load_cols<T, VEC, NC>(x + t * a.x_stride + h * a.dim, k.col, in, u);
+    load_cols<T, VEC, NC>(x + at.t * a.x_stride + at.h * a.dim, k.col, in, u);
     if constexpr (MODE != kModeNone) {
-      load_cols<T, VEC, NC>(z + t * a.z_stride + h * a.dim, k.col, in, g);
+      load_cols<T, VEC, NC>(z + at.t * a.z_stride + at.h * a.dim, k.col, in, g);
 #pragma unroll
       for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -158,7 +187,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void norm_fwd_kernel(
         if (bias) y[e] += b[i][e];
         if constexpr (MODE == kModeLast) y[e] *= g[i][e];
       }
-      store_vec<VEC>(out + row * (int64_t)a.dim + k.col[i], y);
+      store_vec<VEC>(out + at.row * a.dim + k.col[i], y);
     }
   }
 }
@@ -182,18 +211,21 @@ __global__ __launch_bounds__(kBlock<TPR>) void norm_bwd_kernel(
   if (bias) load_cols<float, VEC, NC>(bias, k.col, k.in, b);
   const int64_t step = (int64_t)gridDim.x * RPB;
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += step) {
-    const int64_t row = r0 + rg;
-    const bool live = row < a.rows;
-    const int64_t t = live ? row / a.heads : 0, h = live ? row - t * a.heads : 0;
+    const RowAt at(r0 + rg, a);
+    const int64_t row = at.row, t = at.t, h = at.h;
     bool in[NC];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) in[i] = k.in[i] && live;
+    for (int i = 0; i < NC; ++i) in[i] = k.in[i] && at.live;
     float u[NC][VEC], d[NC][VEC], zz[NC][VEC];
-    load_cols<T, VEC, NC>(x + t * a.x_stride + h * a.dim, k.col, in, u);
-    load_cols<T, VEC, NC>(dout + row * (int64_t)a.dim, k.col, in, d);
-    float xx[MODE == kModeFirst ? NC : 1][VEC];
+    Raw<T, VEC> xr[NC], dr[NC], zr[NC];
+    load_raw<T, VEC, NC>(x + t * a.x_stride + h * a.dim, k.col, in, xr);
+    load_raw<T, VEC, NC>(dout + row * (int64_t)a.dim, k.col, in, dr);
     if constexpr (MODE != kModeNone)
-      load_cols<T, VEC, NC>(z + t * a.z_stride + h * a.dim, k.col, in, zz);
+      load_raw<T, VEC, NC>(z + t * a.z_stride + h * a.dim, k.col, in, zr);
+    unpack<T, VEC, NC>(xr, u);
+    unpack<T, VEC, NC>(dr, d);
+    if constexpr (MODE != kModeNone) unpack<T, VEC, NC>(zr, zz);
+    float xx[MODE == kModeFirst ? NC : 1][VEC];
     if constexpr (MODE == kModeFirst) {
 #pragma unroll
       for (int i = 0; i < NC; ++i)
@@ -258,7 +290,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void norm_bwd_kernel(
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           pw[k.col[i] + e] = dw[i][e];
-          pw[a.dim + k.col[i] + e] = db[i][e];
+          if (bias) pw[a.dim + k.col[i] + e] = db[i][e];
         }
       }
   } else {
@@ -266,6 +298,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void norm_bwd_kernel(
     __shared__ float s_part[RPB * W];
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
+      if (which && !bias) break;
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < NC; ++i)
@@ -324,24 +357,28 @@ Pick pick(const NormShape& s) {
   if (n <= 32) return {32, 1};
   if (n <= 64) return {64, 1};
   if (n <= 128) return {64, 2};
-  if (n <= 256) return {64, 4};
+  if (n <= 256) return {256, 1};  // more vectors a thread spill in the gated gradients
   if (n <= 512) return {256, 2};
-  if (n <= 1024) return {256, 4};
+  if (n <= 1024) return {512, 2};
+  if (n <= 2048) return {1024, 2};
   if (n <= 4096) return {1024, 4};
   return {1024, 16};  // element by element up to 16384
 }
 
 int rows_per_block(const Pick& p) { return p.tpr > 256 ? 1 : 256 / p.tpr; }
 
-// Workgroups of a launch: enough to fill the device a few times over, the rest of the rows in
-// the kernel's loop, which keeps the weights (and the gradients' sums) in registers.
+// Workgroups of a launch; the rest of the rows in the kernel's loop, which keeps the weights (and
+// the gradients' sums) in registers. Forward: the more the better (33860 x 32 rows of 128, gated:
+// 159 us with 16384, 168 with 4096; the next row's loads ahead of this row's work took 169). Backward:
+// each writes a partial row of dweight and dbias, and 768 are what the device holds (16384 rows of
+// 4096: 107 us with 768 and with 1024, 111 with 512; heads of 128: 69, 71 and 77).
 int64_t fwd_blocks(const NormShape& s, const Pick& p) {
   const int64_t all = cdiv(s.N * s.heads, rows_per_block(p));
-  return all < 4096 ? all : 4096;
+  return all < 16384 ? all : 16384;
 }
 int64_t bwd_blocks(const NormShape& s, const Pick& p) {
   const int64_t all = cdiv(s.N * s.heads, rows_per_block(p));
-  const int64_t most = p.tpr > 256 ? 256 : 1024;
+  const int64_t most = p.tpr > 512 ? 256 : p.tpr > 256 ? 512 : 768;
   return all < most ? all : most;
 }
 
@@ -393,11 +430,13 @@ hipError_t bwd_k(const NormShape& s, int64_t blocks, const void* x, const float*
     case 3201: return F<T, VEC, 32, 1>(__VA_ARGS__);                  \
     case 6401: return F<T, VEC, 64, 1>(__VA_ARGS__);                  \
     case 6402: return F<T, VEC, 64, 2>(__VA_ARGS__);                  \
-    case 6404: return F<T, VEC, 64, 4>(__VA_ARGS__);                  \
+    case 25601: return F<T, VEC, 256, 1>(__VA_ARGS__);                \
     case 25602: return F<T, VEC, 256, 2>(__VA_ARGS__);                \
-    case 25604: return F<T, VEC, 256, 4>(__VA_ARGS__);                \
-    case 102404: return F<T, VEC, 1024, 4>(__VA_ARGS__);              \
+    case 51202: return F<T, VEC, 512, 2>(__VA_ARGS__);                \
+    case 102402: return F<T, VEC, 1024, 2>(__VA_ARGS__);              \
   }                                                                   \
+  if constexpr (VEC < 8)                                              \
+    if (p.tpr == 1024 && p.nc == 4) return F<T, VEC, 1024, 4>(__VA_ARGS__);                                                                   \
   if constexpr (VEC == 1)                                             \
     if (p.tpr == 1024 && p.nc == 16) return F<T, VEC, 1024, 16>(__VA_ARGS__); \
   return hipErrorInvalidValue

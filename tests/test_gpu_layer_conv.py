@@ -6,8 +6,8 @@ evaluation (exponential with argument error |x| u and two steps, reciprocal one 
 costs (8 + 2 |pre|) u relative; then one rounding to the output type. Gradients: g = dout
 silu'(pre) moves by at most 0.5 per unit of pre, so by (W + 12) u |dout| (1.1 + 0.5 M) altogether
 (the oracle's magnitudes hold that factor); sums over W taps add W u, sums over tokens at most
-one u per step of the longest chain of additions (64 tokens of a run, 8 runs, one partial row per
-64 .. 512 tokens, added 8 chains wide)."""
+one u per step of the longest chain of additions (128 tokens of a run, 4 runs, one partial row per
+32 or more tokens, added 8 chains wide)."""
 import numpy as np
 import pytest
 
@@ -164,7 +164,7 @@ def test_conv_backward(dtype, dout_dtype, lengths, dims):
                      dstate64, silu)
     assert before is None or torch.equal(before, c["pool"])
     assert set(g) == {"dx", "dweight"} | ({"dbias"} if bias else set()) | ({"dstate0"} if stateful else set())
-    chain = 64 + 8 + n / 64 / 8 + 1
+    chain = 128 + 4 + n / 32 / 8 + 1
     what = f"conv bwd {dtype}/{dout_dtype} W={w} {lengths} {dims}"
     live = np.ones(n, bool)
     if lengths == "ragged":
