@@ -21,9 +21,9 @@
 // join is one multiply-add per state entry and piece.
 //
 // Precision: bf16 inputs enter the products as they are. The decayed x of the state's update are
-// pairs of bf16 (hi + lo, at most 2^-17 off), since states are fp32 results; the decayed scores
-// and the state that S C reads are one bf16 each (2^-8 of a term: the output is rounded by as
-// much). For fp32 inputs every operand is three bf16 (24 bits) and a product takes the six pairs
+// three bf16 (24 bits), since states are fp32 results; the decayed scores and the state that S C
+// reads are one bf16 each (2^-8 of a term: the output is rounded by as much), and so are the
+// decayed x where a piece's state is only formed to be read so. For fp32 inputs every operand is three bf16 (24 bits) and a product takes the six pairs
 // of parts that reach 2^-24: 2.7 times the rate of the fp32 matrix instructions.
 // Gates and their sums are fp32 (the sums of fp32 inputs fp64), and exponents are only taken of
 // differences that are not positive, so strong decays underflow to zero and nothing overflows.
@@ -343,7 +343,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
   constexpr bool F32 = sizeof(T) == 4, OUT = MODE != kState;
   constexpr int NP = D::NP;
   // ... of the update's decayed x: the state of a piece's outputs is only read by S C
-  constexpr int NU = F32 ? 3 : MODE == kOutput ? 1 : 2;
+  constexpr int NU = !F32 && MODE == kOutput ? 1 : 3;
   constexpr int NT = CH / 16, NK = CH / 32;      // token tiles, k steps over tokens
   constexpr int NS = DK / 16, NKS = DK / 32;     // state tiles, k steps over state entries
   constexpr int TRI = NT == 4 ? 3 : 1;           // tiles of scores for a wave at most
@@ -640,9 +640,9 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
     // outputs: the state before decays over the chunk; a piece's state: the chunk's part decays
     // over those behind it
     const float eGn = OUT ? exp2_(gt.total[0]) : exp2_(behind[hw]);
-    bfrag xw[NU][2][NK];
 #pragma unroll
-    for (int k = 0; k < NK; ++k)
+    for (int k = 0; k < NK; ++k) {
+      bfrag xw[NU][2];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float w = gt.w[32 * k + kperm(g, e)];
@@ -655,24 +655,24 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
           __bf16 part[NU];
           split<NU>(v * w, part);
 #pragma unroll
-          for (int p = 0; p < NU; ++p) xw[p][pt][k][e] = part[p];
+          for (int p = 0; p < NU; ++p) xw[p][pt][e] = part[p];
         }
       }
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
+      for (int s = 0; s < NS; ++s) {
 #pragma unroll
-      for (int pt = 0; pt < 2; ++pt)
-        if constexpr (OUT) st[s][pt] *= eGn;
-#pragma unroll
-      for (int k = 0; k < NK; ++k)
+        for (int pt = 0; pt < 2; ++pt)
+          if constexpr (OUT)
+            if (k == 0) st[s][pt] *= eGn;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           const bfrag b = frag_col(s_b + p * kTileB, LDB, 16 * s, k, g, r);
 #pragma unroll
           for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
-            for (int q = 0; q + p < NU; ++q) st[s][pt] = mma_bf16(b, xw[q][pt][k], st[s][pt]);
+            for (int q = 0; q + p < NU; ++q) st[s][pt] = mma_bf16(b, xw[q][pt], st[s][pt]);
         }
+      }
     }
     if constexpr (!OUT) {
       bool more = false;

@@ -401,9 +401,8 @@ gdn_status_t gdn_conv_bwd(const void* x, const float* weight, const float* bias,
  * or 256 each), num_qk_heads the groups that share B and C, and flags 0:
  *   C, B [N, H, dk], x, out [N, HV, dv] in qkv_dtype; dt [N, HV] fp32; A_log, dt_bias [HV] fp32;
  *   D [HV] fp32 or NULL for zero; state_pool [pool, HV, dv, dk] fp32, updated in place.
- * Evaluated in chunks on the matrix cores with fp32 sums: bf16 inputs keep 16 bits or more in
- * every factor of the states and one bf16 rounding in each factor of the outputs, fp32 inputs 24
- * bits in both. A non-finite x also reaches that column of the up to 31 tokens before it in its
+ * Evaluated in chunks on the matrix cores with fp32 sums: every factor keeps 24 bits in the
+ * states, and in the outputs of fp32 inputs; one bf16 rounding in the outputs of bf16 inputs. A non-finite x also reaches that column of the up to 31 tokens before it in its
  * request.
  * C, B, x, out and state_pool 16-byte aligned. workspace: at least gdn_ssm_workspace_size bytes,
  * 256-byte aligned; its contents on entry do not matter. N == 0 or B == 0 is a no-op. */
