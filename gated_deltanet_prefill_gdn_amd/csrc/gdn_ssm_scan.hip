@@ -157,13 +157,17 @@ __device__ __forceinline__ float softplusf(float x) {
   return fmaxf(x, 0.f) + (w == 1.f ? z : l);
 }
 
-// v as a sum of P bf16: 2^-8, 2^-17 or 2^-25 of v off.
+// a and b as sums of P bf16 each (2^-8, 2^-17 or 2^-25 of them off), the parts of the two side by
+// side in a register: one conversion instruction takes both.
 template <int P>
-__device__ __forceinline__ void split(float v, __bf16 (&part)[P]) {
+__device__ __forceinline__ void split(float a, float b, uint32_t (&part)[P]) {
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    part[p] = (__bf16)v;
-    v -= (float)part[p];
+    part[p] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+    if (p + 1 < P) {
+      a -= __uint_as_float(part[p] << 16);
+      b -= __uint_as_float(part[p] & 0xFFFF0000u);
+    }
   }
 }
 
@@ -280,17 +284,12 @@ struct Stage {
         }
       } else {
         const f32x4 v = __builtin_bit_cast(f32x4, r[i]);
-        bf16x4 part[NP];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          __bf16 one[NP];
-          split<NP>(v[e], one);
-#pragma unroll
-          for (int p = 0; p < NP; ++p) part[p][e] = one[p];
-        }
+        uint32_t lo[NP], hi[NP];
+        split<NP>(v[0], v[1], lo);
+        split<NP>(v[2], v[3], hi);
 #pragma unroll
         for (int p = 0; p < NP; ++p)
-          *reinterpret_cast<bf16x4*>(to + p * plane + row * ld + c) = part[p];
+          *reinterpret_cast<u32x2*>(to + p * plane + row * ld + c) = u32x2{lo[p], hi[p]};
       }
     }
   }
@@ -403,7 +402,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
   const float dskip = a.D ? a.D[hv] : 0.f;
   float behind[kHeads] = {};  // a piece's state: sum of g over the chunks walked, of each head
 
-  Stage<T, CH, DK> qb, qc;
+  Stage<T, CH, DK> qb, qc;  // the next chunk's rows (two chunks ahead are no faster)
   Stage<T, CH, kColsBlock> qx;
   float qdt = 0.f;
   auto fetch = [&](int64_t t) {
@@ -495,7 +494,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
       for (int i = 0; i < TRI; ++i) {
         int tt, jt;
         if (!deal<NT>(wv, i, tt, jt)) break;
-        acc4 sc = {0.f, 0.f, 0.f, 0.f};
+        acc4 half[2] = {acc4{0.f, 0.f, 0.f, 0.f}, acc4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int k = 0; k < NKS; ++k)
 #pragma unroll
@@ -505,10 +504,11 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
             const bfrag c = bfrag_of(cp[0], cp[1]);
 #pragma unroll
             for (int q = 0; q + p < NP; ++q)
-              sc = mma_bf16(*reinterpret_cast<const bfrag*>(s_b + q * kTileB + (16 * jt + r) * LDB +
-                                                            32 * k + 8 * g),
-                            c, sc);
+              half[k % 2] = mma_bf16(
+                  *reinterpret_cast<const bfrag*>(s_b + q * kTileB + (16 * jt + r) * LDB + 32 * k + 8 * g),
+                  c, half[k % 2]);
           }
+        const acc4 sc = half[0] + half[1];
         for (int hh = 0; hh < nh; ++hh) {
           const G& gs = gate_set(hh, chunk);
           float v[4];
@@ -526,32 +526,32 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
               v[e] = 4 * g + e <= r ? sc[e] * ex : 0.f;
             }
           }
-          bf16x4 part[NP];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            __bf16 one[NP];
-            split<NP>(v[e], one);
-#pragma unroll
-            for (int p = 0; p < NP; ++p) part[p][e] = one[p];
-          }
+          uint32_t lo[NP], hi[NP];
+          split<NP>(v[0], v[1], lo);
+          split<NP>(v[2], v[3], hi);
 #pragma unroll
           for (int p = 0; p < NP; ++p)
-            *reinterpret_cast<bf16x4*>(s_p + (hh * NP + p) * kTileP + (16 * tt + r) * LDP +
-                                       32 * (jt / 2) + 8 * g + 4 * (jt % 2)) = part[p];
+            *reinterpret_cast<u32x2*>(s_p + (hh * NP + p) * kTileP + (16 * tt + r) * LDP +
+                                      32 * (jt / 2) + 8 * g + 4 * (jt % 2)) = u32x2{lo[p], hi[p]};
         }
       }
       // S^T as the operand of S C: formed once for the chunk's token tiles, or, where there are
       // but two of them, in their loop
       auto state_operand = [&](int k, bfrag (&sb)[NP][2]) {
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt)
+        for (int pt = 0; pt < 2; ++pt) {
+          u32x4 words[NP];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            __bf16 part[NP];
-            split<NP>(st[2 * k + e / 4][pt][e % 4], part);
+          for (int e = 0; e < 8; e += 2) {
+            uint32_t part[NP];
+            const acc4 v = st[2 * k + e / 4][pt];
+            split<NP>(v[e % 4], v[e % 4 + 1], part);
 #pragma unroll
-            for (int p = 0; p < NP; ++p) sb[p][pt][e] = part[p];
+            for (int p = 0; p < NP; ++p) words[p][e / 2] = part[p];
           }
+#pragma unroll
+          for (int p = 0; p < NP; ++p) sb[p][pt] = bf16x8_from_u32x4(words[p]);
+        }
       };
       bfrag sbs[NK > 1 ? NKS : 1][NP][2];
       if constexpr (NK > 1) {
@@ -609,12 +609,12 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 #pragma unroll
             for (int pt = 0; pt < 2; ++pt) {
               const int at = row * LDX + kColsWave * wv + 16 * pt + 4 * g;
-              float xv[4] = {0.f, 0.f, 0.f, 0.f}, o[4];
+              float xv[4], o[4];
 #pragma unroll
               for (int p = NP - 1; p >= 0; --p) {
                 const bf16x4 xp = *reinterpret_cast<const bf16x4*>(s_x + p * kTileX + at);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) xv[i] += (float)xp[i];
+                for (int i = 0; i < 4; ++i) xv[i] = p == NP - 1 ? (float)xp[i] : xv[i] + (float)xp[i];
               }
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -642,35 +642,49 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
     const float eGn = OUT ? exp2_(gt.total[0]) : exp2_(behind[hw]);
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
-      bfrag xw[NU][2];
+      u32x4 xw[NU][2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float w = gt.w[32 * k + kperm(g, e)];
-        if constexpr (!OUT) w *= eGn;
+      for (int e = 0; e < 8; e += 2) {
+        float w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          w[i] = gt.w[32 * k + kperm(g, e + i)];
+          if constexpr (!OUT) w[i] *= eGn;
+        }
 #pragma unroll
         for (int pt = 0; pt < 2; ++pt) {
-          float v = 0.f;
+          float v[2];
 #pragma unroll
-          for (int p = NP - 1; p >= 0; --p) v += (float)xf[p][pt][k][e];
-          __bf16 part[NU];
-          split<NU>(v * w, part);
+          for (int i = 0; i < 2; ++i) {
+            v[i] = (float)xf[NP - 1][pt][k][e + i];
 #pragma unroll
-          for (int p = 0; p < NU; ++p) xw[p][pt][e] = part[p];
+            for (int p = NP - 2; p >= 0; --p) v[i] += (float)xf[p][pt][k][e + i];
+          }
+          uint32_t part[NU];
+          split<NU>(v[0] * w[0], v[1] * w[1], part);
+#pragma unroll
+          for (int p = 0; p < NU; ++p) xw[p][pt][e / 2] = part[p];
         }
       }
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
+      for (int s = 0; s < NS; s += 2) {  // two tiles: four sums between two products of one
+        if constexpr (OUT)
+          if (k == 0)
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt)
-          if constexpr (OUT)
-            if (k == 0) st[s][pt] *= eGn;
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int pt = 0; pt < 2; ++pt) st[s + i][pt] *= eGn;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          const bfrag b = frag_col(s_b + p * kTileB, LDB, 16 * s, k, g, r);
+          bfrag b[2];
 #pragma unroll
-          for (int pt = 0; pt < 2; ++pt)
+          for (int i = 0; i < 2; ++i) b[i] = frag_col(s_b + p * kTileB, LDB, 16 * (s + i), k, g, r);
 #pragma unroll
-            for (int q = 0; q + p < NU; ++q) st[s][pt] = mma_bf16(b, xw[q][pt], st[s][pt]);
+          for (int q = 0; q + p < NU; ++q)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int pt = 0; pt < 2; ++pt) st[s + i][pt] = mma_bf16(b[i], bf16x8_from_u32x4(xw[q][pt]), st[s + i][pt]);
         }
       }
     }
