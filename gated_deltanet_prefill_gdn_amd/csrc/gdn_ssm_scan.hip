@@ -360,8 +360,8 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
   const int vc = a.rep * a.dv;
   const int ncols = vc - col0 < kColsBlock ? vc - col0 : kColsBlock;
 
-  const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int r = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int lane = tid & 63, r = lane & 15, g = lane >> 4;
   const bool live = kColsWave * wv < ncols;
   const int wcol = live ? col0 + kColsWave * wv : col0;
   const int hv = h * a.rep + wcol / a.dv, p0 = wcol % a.dv;
@@ -436,6 +436,13 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 
   for (int chunk = 0; chunk < chunks; ++chunk) {
     const int64_t t0 = place(chunk);
+    if constexpr (MODE == kWhole) {
+      // Places in LDS are formed anew for every chunk: kept in registers they spill, and a
+      // reload waits for the next chunk's rows, which were asked for before it.
+      asm volatile("" : "+v"(lane));
+      r = lane & 15;
+      g = lane >> 4;
+    }
     if (chunk > 0) __syncthreads();  // the chunk before has been read
     const int rows = sg.t1 - t0 < CH ? (int)(sg.t1 - t0) : CH;
     qb.template store<NP, true>(s_b, kTileB, LDB);
