@@ -14,13 +14,17 @@ namespace layer {
 namespace {
 
 constexpr int kTokenThreads = 256;
-// A workgroup covers 64 rows at dk = 64 and 128 and 32 at dk = 256: a divisor of every dv.
-template <int DK>
-constexpr int kRowsPerThread = DK == 64 ? 2 : 4;
-template <int DK>
-constexpr int kRowsPerBlock = (64 / (DK / 8)) * kRowsPerThread<DK> * (kTokenThreads / 64);
-static_assert(kRowsPerBlock<64> == 64 && kRowsPerBlock<128> == 64 && kRowsPerBlock<256> == 32,
-              "a workgroup's rows divide dv");
+// Rows of a lane group. For one token two keep enough state loads in flight (512 requests, 32
+// heads of 128 x 128: 369 us, 5.9 TB/s, with two, 400 with four, 565 with one); with several
+// tokens four share each load of B and C (four tokens: 405 us, 460 with two).
+template <int DK, bool ONE>
+constexpr int kRows = ONE || DK == 64 ? 2 : 4;
+template <int DK, bool ONE>
+constexpr int kRowsPerBlock = (64 / (DK / 8)) * kRows<DK, ONE> * (kTokenThreads / 64);
+static_assert(kRowsPerBlock<64, false> == 64 && kRowsPerBlock<128, false> == 64 &&
+                  kRowsPerBlock<256, false> == 32 && kRowsPerBlock<64, true> == 64 &&
+                  kRowsPerBlock<128, true> == 32 && kRowsPerBlock<256, true> == 16,
+              "a workgroup's rows divide dv (64, 128 or 256)");
 
 __device__ __forceinline__ float softplusf(float x) {
   return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
@@ -68,8 +72,8 @@ __device__ __forceinline__ void load8(const __bf16* row, int gl, float (&x)[8]) 
   }
 }
 
-// cu == nullptr: one token per request, row b.
-template <int DK, typename T>
+// ONE: one token per request, row b (cu is not read).
+template <int DK, typename T, bool ONE>
 __global__ __launch_bounds__(kTokenThreads) void ssm_token_kernel(
     const T* __restrict__ cm, const T* __restrict__ bm, const T* __restrict__ x,
     const float* __restrict__ dt, const float* __restrict__ A_log,
@@ -77,20 +81,20 @@ __global__ __launch_bounds__(kTokenThreads) void ssm_token_kernel(
     float* __restrict__ state_pool, const int64_t* __restrict__ idx,
     const int64_t* __restrict__ cu, T* __restrict__ out, int64_t N, int64_t pool, int H, int HV,
     int DV, int nrb, int64_t max_len) {
-  constexpr int LPR = DK / 8, RPW = 64 / LPR, NR = kRowsPerThread<DK>, RWV = RPW * NR;
+  constexpr int LPR = DK / 8, RPW = 64 / LPR, NR = kRows<DK, ONE>, RWV = RPW * NR;
   const uint32_t pair = blockIdx.x / (uint32_t)nrb;
   const int rb = (int)(blockIdx.x - pair * (uint32_t)nrb);
   const uint32_t b = pair / (uint32_t)HV;
   const int hv = (int)(pair - b * (uint32_t)HV), h = hv / (HV / H);
   int64_t t = b, t_end = (int64_t)b + 1;
-  if (cu) {
+  if constexpr (!ONE) {
     t = cu[b] < 0 ? 0 : cu[b];
     t_end = cu[b + 1] < N ? cu[b + 1] : N;
   }
   const int64_t slot = idx[b];
   if (t >= t_end || t_end - t > max_len || slot < 0 || slot >= pool) return;
   const int l = threadIdx.x & 63, gl = l % LPR;
-  const int r0 = rb * kRowsPerBlock<DK> + (threadIdx.x >> 6) * RWV + l / LPR;
+  const int r0 = rb * kRowsPerBlock<DK, ONE> + (threadIdx.x >> 6) * RWV + l / LPR;
   float* const sp = state_pool + ((slot * HV + hv) * (int64_t)DV + r0) * DK + 4 * gl;
   f32x4 s[NR][2];
 #pragma unroll
@@ -129,32 +133,39 @@ __global__ __launch_bounds__(kTokenThreads) void ssm_token_kernel(
   }
 }
 
-int rows_per_block(int dk) { return dk == 256 ? kRowsPerBlock<256> : kRowsPerBlock<128>; }
+int rows_per_block(int dk, bool one) {
+  return dk == 256 ? (one ? kRowsPerBlock<256, true> : kRowsPerBlock<256, false>)
+         : dk == 128 ? (one ? kRowsPerBlock<128, true> : kRowsPerBlock<128, false>)
+                     : kRowsPerBlock<64, true>;
+}
 
-int64_t token_blocks(const SsmShape& s) { return s.B * s.HV * (s.dv / rows_per_block(s.dk)); }
+int64_t token_blocks(const SsmShape& s, bool one) {
+  return s.B * s.HV * (s.dv / rows_per_block(s.dk, one));
+}
 
-template <int DK, typename T>
+template <int DK, typename T, bool ONE>
 hipError_t launch_token(const SsmShape& s, const void* C, const void* B, const void* x,
                         const float* dt, const float* A_log, const float* dt_bias, const float* D,
                         float* state, const int64_t* idx, const int64_t* cu, void* out,
                         int64_t max_len, hipStream_t st) {
-  hipLaunchKernelGGL((ssm_token_kernel<DK, T>), dim3((unsigned)token_blocks(s)),
+  hipLaunchKernelGGL((ssm_token_kernel<DK, T, ONE>), dim3((unsigned)token_blocks(s, ONE)),
                      dim3(kTokenThreads), 0, st, (const T*)C, (const T*)B, (const T*)x, dt, A_log,
                      dt_bias, D, state, idx, cu, (T*)out, s.N, s.pool, s.H, s.HV, s.dv,
-                     s.dv / kRowsPerBlock<DK>, max_len);
+                     s.dv / kRowsPerBlock<DK, ONE>, max_len);
   return hipGetLastError();
 }
 
+template <bool ONE>
 hipError_t launch_token_any(const SsmShape& s, const void* C, const void* B, const void* x,
                             const float* dt, const float* A_log, const float* dt_bias,
                             const float* D, float* state, const int64_t* idx, const int64_t* cu,
                             void* out, int64_t max_len, hipStream_t st) {
-#define GDN_SSM_CASE(DK)                                                                        \
-  if (s.dk == DK)                                                                               \
-    return s.bf16 ? launch_token<DK, __bf16>(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu, \
-                                             out, max_len, st)                                  \
-                  : launch_token<DK, float>(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu,  \
-                                            out, max_len, st);
+#define GDN_SSM_CASE(DK)                                                                     \
+  if (s.dk == DK)                                                                            \
+    return s.bf16 ? launch_token<DK, __bf16, ONE>(s, C, B, x, dt, A_log, dt_bias, D, state,  \
+                                                  idx, cu, out, max_len, st)                 \
+                  : launch_token<DK, float, ONE>(s, C, B, x, dt, A_log, dt_bias, D, state,   \
+                                                 idx, cu, out, max_len, st);
   GDN_SSM_CASE(64)
   GDN_SSM_CASE(128)
   GDN_SSM_CASE(256)
@@ -164,20 +175,22 @@ hipError_t launch_token_any(const SsmShape& s, const void* C, const void* B, con
 
 }  // namespace
 
-bool ssm_token_grid_fits(const SsmShape& s) { return grid_ok(token_blocks(s), kTokenThreads); }
+bool ssm_token_grid_fits(const SsmShape& s) {
+  return grid_ok(token_blocks(s, true), kTokenThreads);  // the larger of the two grids
+}
 
 hipError_t launch_ssm_decode(const SsmShape& s, const void* C, const void* B, const void* x,
                              const float* dt, const float* A_log, const float* dt_bias,
                              const float* D, float* state, const int64_t* idx, void* out,
                              hipStream_t st) {
-  return launch_token_any(s, C, B, x, dt, A_log, dt_bias, D, state, idx, nullptr, out, 1, st);
+  return launch_token_any<true>(s, C, B, x, dt, A_log, dt_bias, D, state, idx, nullptr, out, 1, st);
 }
 
 hipError_t launch_ssm_short(const SsmShape& s, const void* C, const void* B, const void* x,
                             const float* dt, const float* A_log, const float* dt_bias,
                             const float* D, float* state, const int64_t* idx, const int64_t* cu,
                             void* out, int64_t max_len, hipStream_t st) {
-  return launch_token_any(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu, out, max_len, st);
+  return launch_token_any<false>(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu, out, max_len, st);
 }
 
 }  // namespace layer

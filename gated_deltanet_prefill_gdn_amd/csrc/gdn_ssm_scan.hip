@@ -23,9 +23,9 @@
 // Precision: bf16 inputs enter the products as they are. The decayed x of the state's update are
 // three bf16 (24 bits), since states are fp32 results; the decayed scores and the state that S C
 // reads are one bf16 each (2^-8 of a term: the output is rounded by as much), and so are the
-// decayed x where a piece's state is only formed to be read so. For fp32 inputs every operand is three bf16 (24 bits) and a product takes the six pairs
-// of parts that reach 2^-24: 2.7 times the rate of the fp32 matrix instructions.
-// Gates and their sums are fp32 (the sums of fp32 inputs fp64), and exponents are only taken of
+// decayed x where a piece's state is only formed to be read so. For fp32 inputs every operand is
+// three bf16 (24 bits) and a product takes the six pairs of parts that reach 2^-24: 2.7 times the
+// rate of the fp32 matrix instructions. Gates and their sums are fp32 (the sums of fp32 inputs fp64), and exponents are only taken of
 // differences that are not positive, so strong decays underflow to zero and nothing overflows.
 #include <type_traits>
 
@@ -799,8 +799,8 @@ int segment_tokens(const SsmShape& s) {
 
 // Requests of at most this many tokens run token by token, where the mean length says that most
 // are and there are enough to fill the device (a call that splits pays a launch for the longer
-// ones too): 512 requests of 4 tokens, 32 heads of 128 x 128, take 382 us there and 483 in chunks,
-// of 8 tokens 559 and 491.
+// ones too): 512 requests of 4 tokens, 32 heads of 128 x 128, take 401 us there, of 8 tokens 559;
+// in chunks requests of 6 take 456 and of 8 454.
 int short_tokens(const SsmShape& s) {
   return s.N <= 4 * s.B && s.B * s.HV * (s.dv / 64) >= 2048 ? 4 : 0;
 }
