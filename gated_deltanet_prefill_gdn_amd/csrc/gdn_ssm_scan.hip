@@ -25,8 +25,9 @@
 // reads are one bf16 each (2^-8 of a term: the output is rounded by as much), and so are the
 // decayed x where a piece's state is only formed to be read so. For fp32 inputs every operand is
 // three bf16 (24 bits) and a product takes the six pairs of parts that reach 2^-24: 2.7 times the
-// rate of the fp32 matrix instructions. Gates and their sums are fp32 (the sums of fp32 inputs fp64), and exponents are only taken of
-// differences that are not positive, so strong decays underflow to zero and nothing overflows.
+// rate of the fp32 matrix instructions. Gates and their sums are fp32 (the sums of fp32 inputs
+// fp64), and exponents are only taken of differences that are not positive, so strong decays
+// underflow to zero and nothing overflows.
 #include <type_traits>
 
 #include "gdn_layer.h"

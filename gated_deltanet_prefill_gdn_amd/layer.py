@@ -98,6 +98,15 @@ def _p(t):
     return t.data_ptr() if t is not None else None
 
 
+def _new(stream, shape, dtype, device):
+    """Memory for an output or a workspace. It belongs to the stream that the call runs on, so
+    that its reuse is ordered with the kernels that write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _call(what, device, stream, fn, *args):
     """The library launches on the current device, so it is made that of the tensors."""
     if device.type != "cuda":
@@ -117,9 +126,9 @@ def _call(what, device, stream, fn, *args):
         raise GdnError(rc, what)
 
 
-def _workspace(workspace, need, device):
+def _workspace(workspace, need, device, stream):
     if workspace is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        return _new(stream, max(need, 1), torch.uint8, device)
     _need(workspace, "workspace", dtype=torch.uint8, ndim=1, device=device)
     return workspace
 
@@ -171,22 +180,22 @@ def _conv_check(x, weight, bias, state_pool, cache_indices, cu_seqlens, dims, si
     _shape(weight, "weight", (ch, w), _F32, x)
     if bias is not None:
         _shape(bias, "bias", (ch,), _F32, x)
-    if state_pool is None and cache_indices is not None and cu_seqlens is None:
+    if state_pool is None and cu_seqlens is None:
         raise ValueError("state_pool is required")
     if state_pool is not None:
         if cache_indices is None:
             raise ValueError("cache_indices are required with a state_pool")
-        _shape(state_pool, "state_pool", (state_pool.shape[0], w - 1, ch), x.dtype, x)
+        _shape(state_pool, "state_pool", state_pool.shape[:1] + (w - 1, ch), x.dtype, x)
     batch = _requests(cache_indices if state_pool is not None else None, cu_seqlens, x)
     prob = conv_problem(x, w, dims, batch, 0 if state_pool is None else state_pool.shape[0], silu,
                         **kw)
     return dev, dims, prob
 
 
-def _conv_outs(outs, x, dims):
+def _conv_outs(outs, x, dims, stream):
     n = x.shape[0]
     if outs is None:
-        return tuple([x.new_empty((n, d)) for d in dims])
+        return tuple([_new(stream, (n, d), x.dtype, x.device) for d in dims])
     if len(outs) != len(dims):
         raise ValueError(f"{len(dims)} outputs are wanted, got {len(outs)}")
     for i, (o, d) in enumerate(zip(outs, dims)):
@@ -212,7 +221,7 @@ def gdn_conv_fwd(x, weight, bias, state_pool, cache_indices, cu_seqlens, dims=No
     outputs are not written."""
     dev, dims, prob = _conv_check(x, weight, bias, state_pool, cache_indices, cu_seqlens, dims,
                                   silu)
-    outs = _conv_outs(outs, x, dims)
+    outs = _conv_outs(outs, x, dims, stream)
     _call("gdn_conv_fwd", dev, stream, load_library().gdn_conv_fwd, _p(x), _p(weight), _p(bias),
           _p(state_pool), _p(cache_indices), _p(cu_seqlens), *_three(outs), ctypes.byref(prob))
     return outs
@@ -222,7 +231,7 @@ def gdn_conv_decode_fwd(x, weight, bias, state_pool, cache_indices, dims=None, s
                         outs=None, stream=None):
     """gdn_conv_fwd for one new token per request: x [B, channels], row b with request b."""
     dev, dims, prob = _conv_check(x, weight, bias, state_pool, cache_indices, None, dims, silu)
-    outs = _conv_outs(outs, x, dims)
+    outs = _conv_outs(outs, x, dims, stream)
     _call("gdn_conv_decode_fwd", dev, stream, load_library().gdn_conv_decode_fwd, _p(x),
           _p(weight), _p(bias), _p(state_pool), _p(cache_indices), *_three(outs),
           ctypes.byref(prob))
@@ -249,7 +258,7 @@ def gdn_conv_bwd(x, weight, bias, state_pool, cache_indices, cu_seqlens, douts, 
         _shape(d, f"douts[{i}]", (n, dims[i]), douts[0].dtype, x)
     ch = x.shape[1] if x.dim() == 2 else 0
     if dx is None:
-        dx = torch.empty((n, ch), dtype=x.dtype, device=dev)
+        dx = _new(stream, (n, ch), x.dtype, dev)
     dev, dims, prob = _conv_check(x, weight, bias, state_pool, cache_indices, cu_seqlens, dims,
                                   silu, dout_dtype=_code(douts[0], "douts"),
                                   dx_stride=_rows(dx, "dx", (ch,), x))
@@ -258,12 +267,12 @@ def gdn_conv_bwd(x, weight, bias, state_pool, cache_indices, cu_seqlens, douts, 
     b, w = prob.batch, prob.width
     if dstate is not None:
         _shape(dstate, "dstate", (b, w - 1, ch), _F32, x)
-    g = {"dx": dx, "dweight": torch.empty((ch, w), dtype=_F32, device=dev)}
+    g = {"dx": dx, "dweight": _new(stream, (ch, w), _F32, dev)}
     if bias is not None:
-        g["dbias"] = torch.empty((ch,), dtype=_F32, device=dev)
+        g["dbias"] = _new(stream, (ch,), _F32, dev)
     if state_pool is not None:
-        g["dstate0"] = torch.empty((b, w - 1, ch), dtype=_F32, device=dev)
-    ws = _workspace(workspace, gdn_conv_bwd_workspace_size(prob), dev)
+        g["dstate0"] = _new(stream, (b, w - 1, ch), _F32, dev)
+    ws = _workspace(workspace, gdn_conv_bwd_workspace_size(prob), dev, stream)
     _call("gdn_conv_bwd", dev, stream, load_library().gdn_conv_bwd, _p(x), _p(weight), _p(bias),
           _p(state_pool), _p(cache_indices), _p(cu_seqlens), *_three(douts), _p(dstate), _p(dx),
           _p(g["dweight"]), _p(g.get("dbias")), _p(g.get("dstate0")), ctypes.byref(prob), _p(ws),
@@ -277,7 +286,8 @@ def gdn_ssm_workspace_size(prob: GdnProblem) -> int:
     return int(load_library().gdn_ssm_workspace_size(ctypes.byref(prob)))
 
 
-def _ssm_check(C, B, x, dt, A_log, dt_bias, D, state_pool, cache_indices, cu_seqlens, out):
+def _ssm_check(C, B, x, dt, A_log, dt_bias, D, state_pool, cache_indices, cu_seqlens, out,
+               stream):
     dev = x.device
     if x.dim() != 3 or B.dim() != 3:
         raise ValueError("x must be [N, HV, dv] and B [N, H, dk]")
@@ -293,12 +303,12 @@ def _ssm_check(C, B, x, dt, A_log, dt_bias, D, state_pool, cache_indices, cu_seq
     _shape(dt_bias, "dt_bias", (hv,), _F32, x)
     if D is not None:
         _shape(D, "D", (hv,), _F32, x)
-    _shape(state_pool, "state_pool", (state_pool.shape[0], hv, dv, dk), _F32, x)
+    _shape(state_pool, "state_pool", state_pool.shape[:1] + (hv, dv, dk), _F32, x)
     batch = _requests(cache_indices, cu_seqlens, x)
     if cu_seqlens is None and batch != n:
         raise ValueError("cache_indices must have one entry per row of x")
     if out is None:
-        out = x.new_empty((n, hv, dv))
+        out = _new(stream, (n, hv, dv), x.dtype, dev)
     else:
         _shape(out, "out", (n, hv, dv), x.dtype, x)
     return dev, out, GdnProblem(n, batch, h, hv, dk, dv, state_pool.shape[0], code, 0)
@@ -315,8 +325,8 @@ def gdn_ssm_prefill_fwd(C, B, x, dt, A_log, dt_bias, D, state_pool, cache_indice
     gdn_ssm_workspace_size bytes. Rows behind cu_seqlens[B], and requests whose cache index is
     outside the pool, are padding: their outputs are not written."""
     dev, out, prob = _ssm_check(C, B, x, dt, A_log, dt_bias, D, state_pool, cache_indices,
-                                cu_seqlens, out)
-    ws = _workspace(workspace, gdn_ssm_workspace_size(prob), dev)
+                                cu_seqlens, out, stream)
+    ws = _workspace(workspace, gdn_ssm_workspace_size(prob), dev, stream)
     _call("gdn_ssm_prefill_fwd", dev, stream, load_library().gdn_ssm_prefill_fwd, _p(C), _p(B),
           _p(x), _p(dt), _p(A_log), _p(dt_bias), _p(D), _p(state_pool), _p(cache_indices),
           _p(cu_seqlens), _p(out), ctypes.byref(prob), _p(ws), ws.numel())
@@ -327,7 +337,7 @@ def gdn_ssm_decode_fwd(C, B, x, dt, A_log, dt_bias, D, state_pool, cache_indices
                        stream=None):
     """One step of the scan, one token per request: row b of every input with request b."""
     dev, out, prob = _ssm_check(C, B, x, dt, A_log, dt_bias, D, state_pool, cache_indices, None,
-                                out)
+                                out, stream)
     _call("gdn_ssm_decode_fwd", dev, stream, load_library().gdn_ssm_decode_fwd, _p(C), _p(B),
           _p(x), _p(dt), _p(A_log), _p(dt_bias), _p(D), _p(state_pool), _p(cache_indices),
           _p(out), ctypes.byref(prob))
@@ -372,7 +382,7 @@ def gdn_norm_fwd(x, weight, bias=None, z=None, eps: float = 1e-6, rms: bool = Tr
     None fp32, shared by the heads; 1 <= dim <= 16384."""
     dev, prob = _norm_check(x, weight, bias, z, eps, rms, gate_first)
     if out is None:
-        out = x.new_empty(x.shape)
+        out = _new(stream, x.shape, x.dtype, x.device)
     else:
         _shape(out, "out", x.shape, x.dtype, x)
     _call("gdn_norm_fwd", dev, stream, load_library().gdn_norm_fwd, _p(x), _p(weight), _p(bias),
@@ -389,18 +399,18 @@ def gdn_norm_bwd(x, weight, bias, z, dout, eps: float = 1e-6, rms: bool = True,
     """Gradients of gdn_norm_fwd: a dict of dx (dense) and, with a gate, dz (``dz``: tokens any
     stride apart) in x's dtype, dweight and, with a bias, dbias, fp32. dout: dense, x's dtype."""
     if z is not None and dz is None:
-        dz = torch.empty(z.shape, dtype=z.dtype, device=z.device)
+        dz = _new(stream, z.shape, z.dtype, z.device)
     elif z is None and dz is not None:
         raise ValueError("dz without a gate z")
     dev, prob = _norm_check(x, weight, bias, z, eps, rms, gate_first, dz)
     _shape(dout, "dout", x.shape, x.dtype, x)
-    g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
-         "dweight": torch.empty(weight.shape, dtype=_F32, device=dev)}
+    g = {"dx": _new(stream, x.shape, x.dtype, dev),
+         "dweight": _new(stream, weight.shape, _F32, dev)}
     if z is not None:
         g["dz"] = dz
     if bias is not None:
-        g["dbias"] = torch.empty(weight.shape, dtype=_F32, device=dev)
-    ws = _workspace(workspace, gdn_norm_bwd_workspace_size(prob), dev)
+        g["dbias"] = _new(stream, weight.shape, _F32, dev)
+    ws = _workspace(workspace, gdn_norm_bwd_workspace_size(prob), dev, stream)
     _call("gdn_norm_bwd", dev, stream, load_library().gdn_norm_bwd, _p(x), _p(weight), _p(bias),
           _p(z), _p(dout), _p(g["dx"]), _p(dz), _p(g["dweight"]), _p(g.get("dbias")),
           ctypes.byref(prob), _p(ws), ws.numel())

@@ -402,8 +402,10 @@ gdn_status_t gdn_conv_bwd(const void* x, const float* weight, const float* bias,
  *   C, B [N, H, dk], x, out [N, HV, dv] in qkv_dtype; dt [N, HV] fp32; A_log, dt_bias [HV] fp32;
  *   D [HV] fp32 or NULL for zero; state_pool [pool, HV, dv, dk] fp32, updated in place.
  * Evaluated in chunks on the matrix cores with fp32 sums: every factor keeps 24 bits in the
- * states, and in the outputs of fp32 inputs; one bf16 rounding in the outputs of bf16 inputs. A non-finite x also reaches that column of the up to 31 tokens before it in its
- * request.
+ * states, and in the outputs of fp32 inputs; one bf16 rounding in the outputs of bf16 inputs.
+ * Long requests are worked on in pieces, whose length goes by N, B and the shape alone. A
+ * non-finite x also reaches that column of the up to 31 tokens before it in its request, and
+ * need not reach the states behind its piece once its decay there is zero in fp32.
  * C, B, x, out and state_pool 16-byte aligned. workspace: at least gdn_ssm_workspace_size bytes,
  * 256-byte aligned; its contents on entry do not matter. N == 0 or B == 0 is a no-op. */
 size_t gdn_ssm_workspace_size(const gdn_problem_t* prob);

@@ -127,18 +127,43 @@ def test_other_stream():
     """On a stream of the caller's, inputs made there; nothing runs on the current one."""
     import gated_deltanet_prefill_gdn_amd as gdn
     s = torch.cuda.Stream()
+    ones = torch.ones(64, device=DEV)
     pool = torch.zeros(3, 4, 64, 128, device=DEV)
     p2, idx, cu = pool.clone(), i64([2, 0]), i64([0, 100, 357])
     c = scan_inputs(3, 357)
     want = gdn.gdn_ssm_prefill_fwd(*c.values(), p2, idx, cu)
-    y2 = gdn.gdn_norm_fwd(want, torch.ones(64, device=DEV))
+    y2 = gdn.gdn_norm_fwd(want, ones)
     torch.cuda.synchronize()
     with torch.cuda.stream(s):
         c2 = {k: v + 0 for k, v in c.items()}
     out = gdn.gdn_ssm_prefill_fwd(*c2.values(), pool, idx, cu, stream=s)
-    y = gdn.gdn_norm_fwd(out, torch.ones(64, device=DEV), stream=s)
+    y = gdn.gdn_norm_fwd(out, ones, stream=s)
     s.synchronize()
     assert torch.equal(out, want) and torch.equal(pool, p2) and torch.equal(y, y2)
+
+
+def test_outputs_belong_to_the_stream_of_the_call():
+    """What a call allocates is memory of the stream it runs on: freed, it is not handed to work
+    of another stream while the kernels still use it."""
+    import gated_deltanet_prefill_gdn_amd as gdn
+    s = torch.cuda.Stream()
+    c, idx, cu = scan_inputs(4, 300), i64([0]), i64([0, 300])
+    pool = torch.zeros(1, 4, 64, 128, device=DEV)
+    x, w = torch.randn(300, 64, device=DEV), torch.randn(64, 4, device=DEV)
+    rows, scale = torch.randn(300, 1, 64, device=DEV), torch.ones(64, device=DEV)
+    torch.cuda.synchronize()
+    made = [gdn.gdn_ssm_prefill_fwd(*c.values(), pool, idx, cu, stream=s),
+            gdn.gdn_conv_fwd(x, w, None, None, None, cu, stream=s)[0],
+            *gdn.gdn_conv_bwd(x, w, None, None, None, cu, (x,), stream=s).values(),
+            gdn.gdn_norm_fwd(rows, scale, stream=s),
+            *gdn.gdn_norm_bwd(rows, scale, None, rows, rows, stream=s).values()]
+    s.synchronize()
+    segments = torch.cuda.memory_snapshot()
+    for t in made:
+        at = t.data_ptr()
+        owner, = [g["stream"] for g in segments
+                  if g["address"] <= at < g["address"] + g["total_size"]]
+        assert owner == s.cuda_stream
 
 
 def test_captured_layer_replays_to_the_eager_result():

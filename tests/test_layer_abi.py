@@ -217,7 +217,8 @@ def test_conv_binding_refusals(kw, err):
 def test_conv_decode_and_backward_binding_refusals():
     a = conv_args()
     a.pop("cu_seqlens")
-    for kw in (dict(state_pool=None), dict(x=z(5, 24)), {}):
+    for kw in (dict(state_pool=None), dict(x=z(5, 24)), {}, dict(state_pool=torch.zeros(())),
+               dict(state_pool=None, cache_indices=None)):
         with pytest.raises((ValueError, gdn.GdnError)):
             gdn.gdn_conv_decode_fwd(**{**a, **kw})
     b = conv_args(douts=(z(6, 8, dtype=F32),) * 3)
