@@ -34,4 +34,5 @@ ASAN_OPTIONS=detect_leaks=0:abort_on_error=1:halt_on_error=1 \
 UBSAN_OPTIONS=print_stacktrace=1:halt_on_error=1 \
 GDN_LIBRARY="$OUT/libgdn_san.so" GDN_ORACLE_LIB="$OUT/libgdn_oracle_san.so" \
   python -m pytest -q -p no:cacheprovider -m "not gpu" \
-    tests/test_abi.py tests/test_oracle_pins.py tests/test_oracle_decode.py 2>&1 | tee "$OUT/pytest.log"
+    tests/test_abi.py tests/test_layer_abi.py tests/test_oracle_pins.py \
+    tests/test_oracle_decode.py 2>&1 | tee "$OUT/pytest.log"

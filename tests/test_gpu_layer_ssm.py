@@ -2,11 +2,9 @@
 
 Tolerances, derived. Let M be the same recurrence over absolute values (the oracle's magnitudes):
 any evaluation that rounds the factors of its products by a relative r is off by at most about
-r M. States are fp32 and every factor of their sums carries at least 16 bits: 2^-16 M covers the
-one split factor of bf16 inputs (a pair of bf16 is 2^-17 off at most: the second part is below
-2^-8 of the value, in a binade whose steps are 2^-16) and as much again for the gates (steps of
-2^-24, exponents below 128 steps) and the fp32 sums; fp32 inputs are split in three and stay far
-below. Outputs: for bf16 inputs the decayed scores and the start state enter the matrix products
+r M. States are fp32 and every factor of their sums is split into three bf16, 2^-24 off: 2^-16 M
+leaves room for the gates (steps of 2^-24, exponents below 128 steps, so 2^-17) and the fp32 sums.
+Outputs: for bf16 inputs the decayed scores and the start state enter the matrix products
 as bf16 (2^-8 each, and their own factors below that), so 2^-8 M + 2^-9 M; for fp32 inputs
 2^-15 M. Then one rounding to the output type."""
 import numpy as np
