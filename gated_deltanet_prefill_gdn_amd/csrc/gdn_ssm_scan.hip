@@ -18,7 +18,9 @@
 // state from zero, a second joins the pieces' states in order into their start states and the
 // final one, and a third forms the outputs of all pieces side by side, and takes the requests that
 // are not cut from start to end. Only the scalar decay per head lies between two pieces, so the
-// join is one multiply-add per state entry and piece.
+// join is one multiply-add per state entry and piece. A piece's state is summed from its end, and
+// only as far back as weights are not zero in fp32: heads that forget fast stop after a few chunks,
+// so long pieces are taken in parts, which spread the slow heads over the device.
 //
 // Precision: bf16 inputs enter the products as they are. The decayed x of the state's update are
 // three bf16 (24 bits), since states are fp32 results; the decayed scores and the state that S C
@@ -55,14 +57,19 @@ struct ScanArgs {
   float* pool;
   const int64_t *idx, *cu;
   void* out;
-  float* seg_state;   // [segments of cut requests][HV][dv][dk]
-  float* seg_decay;   // [segments of cut requests][HV]: sum of g over the segment
+  float* seg_state;   // [segments of cut requests][parts][HV][dv][dk]: the parts' states, then in
+                      // the first part's place the segment's start state
+  float* seg_decay;   // [segments of cut requests][parts][HV]: sum of g from a part's start to the
+                      // segment's end, kNoState where the part's state is zero and not written
   int64_t N, nreq, npool;
   int H, HV, dv, rep, blocks_per_group;
   int lseg;           // tokens of a segment (a multiple of 64), 0: nothing is cut
   int max_cut;        // places in seg_state
+  int parts;          // of a segment, whose states are formed side by side
   int short_len;      // requests of at most this many tokens are left to the token kernel
 };
+
+constexpr float kNoState = 1.f;  // (sums of g are not positive)
 
 // Pieces of a request of L tokens, and the tokens of one (a multiple of 64; the last piece may be
 // shorter): as equal as they come, at most lseg. An empty request counts one piece, which has
@@ -334,9 +341,10 @@ struct Dims {
   static_assert(AtX % 16 == 0 && AtG % 16 == 0 && AtC % 16 == 0 && AtP % 16 == 0, "16-byte rows");
 };
 
+// A piece's state: sg is the part of the piece, `ws` its place and `end` the piece's end.
 template <typename T, int DK, int CH, Mode MODE>
 __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& sg, int in_seg,
-                                             char* lds) {
+                                             char* lds, int64_t ws = 0, int64_t end = 0) {
   using D = Dims<T, DK, CH>;
   using R = typename D::R;
   using G = typename D::G;
@@ -388,7 +396,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
   const float* from = nullptr;
   const int64_t plane = (int64_t)a.dv * DK;
   if (OUT) {
-    from = MODE == kOutput ? a.seg_state + ((int64_t)sg.ws * a.HV + hv) * plane
+    from = MODE == kOutput ? a.seg_state + ((int64_t)sg.ws * a.parts * a.HV + hv) * plane
                         : a.pool + (slot * a.HV + hv) * plane;
     from += (int64_t)(p0 + r) * DK + 4 * g;
   }
@@ -401,7 +409,42 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 
   const float decay = -expf(a.A_log[hv0 + gh]) * kLog2e, dtb = a.dt_bias[hv0 + gh];
   const float dskip = a.D ? a.D[hv] : 0.f;
-  float behind[kHeads] = {};  // a piece's state: sum of g over the chunks walked, of each head
+  // a piece's state: sum of g from the chunks walked to the piece's end, of each head
+  float behind[kHeads] = {};
+  if constexpr (MODE == kState) {
+    float* const s_sum = reinterpret_cast<float*>(lds);
+    bool more = sg.t0 < sg.t1;
+    for (int64_t t = sg.t1; more && t < end; t += 4 * kThreads) {
+      float sum[kHeads] = {};
+#pragma unroll
+      for (int hh = 0; hh < kHeads; ++hh) {
+        if (hh >= nh) break;
+        const float rate = -expf(a.A_log[hv0 + hh]) * kLog2e, shift = a.dt_bias[hv0 + hh];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int64_t k = t + u * kThreads + tid;
+          if (k < end) sum[hh] += rate * softplusf(a.dt[k * a.HV + hv0 + hh] + shift);
+        }
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) sum[hh] += __shfl_xor(sum[hh], off, 64);
+        if (lane == 0) s_sum[hh * kWaves + wv] = sum[hh];
+      }
+      __syncthreads();
+      more = false;
+#pragma unroll
+      for (int hh = 0; hh < kHeads; ++hh)
+        if (hh < nh) {
+#pragma unroll
+          for (int k = 0; k < kWaves; ++k) behind[hh] += s_sum[hh * kWaves + k];
+          more = more || !(exp2_(behind[hh]) == 0.f);
+        }
+      __syncthreads();
+    }
+    if (!more) {  // no token, or every weight is zero in fp32
+      if (live && p0 == 0 && lane == 0) a.seg_decay[ws * a.HV + hv] = kNoState;
+      return;
+    }
+  }
 
   Stage<T, CH, DK> qb, qc;  // the next chunk's rows (two chunks ahead are no faster)
   Stage<T, CH, kColsBlock> qx;
@@ -710,14 +753,14 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 
   if (!live || MODE == kOutput) return;
   float* to = MODE == kWhole ? a.pool + (slot * a.HV + hv) * plane
-                             : a.seg_state + ((int64_t)sg.ws * a.HV + hv) * plane;
+                             : a.seg_state + (ws * a.HV + hv) * plane;
   to += (int64_t)(p0 + r) * DK + 4 * g;
 #pragma unroll
   for (int s = 0; s < NS; ++s)
 #pragma unroll
     for (int pt = 0; pt < 2; ++pt)
       *reinterpret_cast<acc4*>(to + 16 * pt * DK + 16 * s) = st[s][pt];
-  if (MODE == kState && p0 == 0 && lane == 0) a.seg_decay[(int64_t)sg.ws * a.HV + hv] = behind[hw];
+  if (MODE == kState && p0 == 0 && lane == 0) a.seg_decay[ws * a.HV + hv] = behind[hw];
 }
 
 // The pieces' states (OUTPUT false); the outputs of pieces, and whole requests.
@@ -729,7 +772,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DK < 256 ? 2 : 1) void 
   // segment to segment, since groups differ in how far a piece's state reaches back.
   const int turn = blockIdx.x / 8, row = turn / a.blocks_per_group;
   const int unit = row * 8 + (blockIdx.x + 3 * row + row / 8) % 8;
-  const int seg = unit / a.H, in_seg = unit % a.H * a.blocks_per_group + turn % a.blocks_per_group;
+  const int in_seg = unit % a.H * a.blocks_per_group + turn % a.blocks_per_group;
+  const int parts = OUTPUT ? 1 : a.parts, seg = unit / a.H / parts;
   if (a.lseg == 0 && seg >= a.nreq) return;  // units are a multiple of eight
   Segment sg;
   if (!find_segment(a, seg, sg)) return;
@@ -739,11 +783,17 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DK < 256 ? 2 : 1) void 
     else
       scan_segment<T, DK, CH, kWhole>(a, sg, in_seg, lds);
   } else if (sg.count > 1) {
-    scan_segment<T, DK, CH, kState>(a, sg, in_seg, lds);
+    const int part = unit / a.H % parts;
+    const int len = ((int)(sg.t1 - sg.t0) + 64 * parts - 1) / (64 * parts) * 64;
+    const int64_t end = sg.t1;
+    sg.t0 += (int64_t)part * len;
+    sg.t1 = sg.t0 + len < end ? sg.t0 + len : end;
+    scan_segment<T, DK, CH, kState>(a, sg, in_seg, lds, (int64_t)sg.ws * parts + part, end);
   }
 }
 
 // Start states of a cut request's pieces, in place of the pieces' own states, and its final state.
+template <int PARTS>
 __global__ __launch_bounds__(256) void ssm_join_kernel(ScanArgs a, int plane, int parts) {
   const int part = blockIdx.x % parts;  // every parts-th run of 1024 entries from this one on
   const int64_t pair = blockIdx.x / parts;
@@ -760,28 +810,57 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(ScanArgs a, int plane, in
     first += __builtin_amdgcn_readlane(wave_inclusive(k > 1 ? k : 0), 63);
   }
   if (first + n > a.max_cut) return;  // cu_seqlens breaks its precondition
-  const float* const d = a.seg_decay + (int64_t)first * a.HV + hv;
+  constexpr int AHEAD = 8 / PARTS;  // pieces whose states are in flight together
   const int64_t step = (int64_t)a.HV * plane;
   for (int e = (part * 256 + threadIdx.x) * 4; e < plane; e += parts * 1024) {
     f32x4* const home = reinterpret_cast<f32x4*>(a.pool + (slot * a.HV + hv) * (int64_t)plane + e);
-    float* p = a.seg_state + ((int64_t)first * a.HV + hv) * plane + e;
+    const float* d = a.seg_decay + (int64_t)first * PARTS * a.HV + hv;
+    float* p = a.seg_state + ((int64_t)first * PARTS * a.HV + hv) * plane + e;
     f32x4 s = *home;
-    for (int i = 0; i < n; ++i, p += step) {
-      const f32x4 mine = *reinterpret_cast<const f32x4*>(p);
-      *reinterpret_cast<f32x4*>(p) = s;
-      s = s * exp2_(d[(int64_t)i * a.HV]) + mine;
+    for (int i = 0; i < n; i += AHEAD, p += AHEAD * PARTS * step, d += AHEAD * PARTS * a.HV) {
+      float G[AHEAD][PARTS];
+      f32x4 mine[AHEAD][PARTS];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+        for (int j = 0; j < PARTS; ++j)
+          G[u][j] = i + u < n ? d[(u * PARTS + j) * a.HV] : kNoState;
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+        for (int j = 0; j < PARTS; ++j) {
+          mine[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (!(G[u][j] > 0.f))
+            mine[u][j] = *reinterpret_cast<const f32x4*>(p + (u * PARTS + j) * step);
+        }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        if (i + u >= n) break;
+        *reinterpret_cast<f32x4*>(p + u * PARTS * step) = s;
+        s *= G[u][0] > 0.f ? 0.f : exp2_(G[u][0]);
+#pragma unroll
+        for (int j = 0; j < PARTS; ++j) s += mine[u][j];
+      }
     }
     *home = s;
   }
 }
 
-// Tokens of a piece at most (0: no request is cut). A workgroup's time goes with its tokens, and
-// `slots` of them run at a time, so pieces are sized to fill k rounds of the device, k N / rounds
+// Tokens of a piece at most (lseg 0: no request is cut). A workgroup's time goes with its tokens,
+// and `slots` of them run at a time, so pieces are sized to fill k rounds of the device, k N / rounds
 // plus half a piece for every request, k = 1 .. 4: more rounds even out pieces of different
 // lengths, fewer spare the joins, which cost what kPieceTokens tokens do (a piece's state is
-// written, joined and read: 256 KB at dk = 128 for 128 columns, whose tokens take 0.75 KB).
-constexpr int kPieceTokens = 350;
-int segment_tokens(const SsmShape& s) {
+// written, joined and read: 256 KB at dk = 128 for 128 columns, whose tokens take 0.75 KB; with 350
+// instead of 1000, 8 ragged requests of 33860 tokens in all, 64 heads of 64 x 128, take 438 us
+// instead of 408, and 16 requests of 1024 are cut for nothing, 140 us instead of 103).
+// A piece's state in one part, two or four, by its length: one request of 131072 tokens, 32 heads
+// of 128 x 128 (pieces of 8512), 367, 317 and 296 us for states and join; pieces of 2880 160, 155
+// and 163; pieces of 1216 174, 192 and 239.
+constexpr int kPieceTokens = 1000;
+struct Cut {
+  int lseg, parts;
+};
+Cut cut_of(const SsmShape& s) {
   const int64_t blocks = cdiv((int64_t)(s.HV / s.H) * s.dv, kColsBlock) * s.H;
   const int64_t slots = s.dk < 256 ? 512 : 256;
   int64_t best = 0, cost = INT64_MAX;
@@ -795,7 +874,8 @@ int segment_tokens(const SsmShape& s) {
     }
   }
   if (best < 512) best = best == 0 ? 0 : 512;
-  return s.N > best ? (int)best : 0;
+  if (best == 0 || s.N <= best) return Cut{0, 1};
+  return Cut{(int)best, best < 2048 ? 1 : best < 4096 ? 2 : 4};
 }
 
 // Requests of at most this many tokens run token by token, where the mean length says that most
@@ -814,33 +894,38 @@ struct ScanLayout {
   size_t state = 0, decay = 0, total = 0;
 };
 ScanLayout scan_layout(const SsmShape& s) {
-  const int64_t n = max_cut(s, segment_tokens(s));
+  const Cut c = cut_of(s);
+  const int64_t n = max_cut(s, c.lseg) * c.parts;
   ScanLayout L;
   L.decay = align256((size_t)n * s.HV * s.dv * s.dk * sizeof(float));
   L.total = L.decay + align256((size_t)n * s.HV * sizeof(float)) + 256;
   return L;
 }
 
-int64_t scan_blocks(const SsmShape& s) {
-  const int lseg = segment_tokens(s);
-  return cdiv((s.B + (lseg ? s.N / lseg : 0)) * s.H, 8) * 8 *
+int64_t scan_blocks(const SsmShape& s, int parts) {
+  const int lseg = cut_of(s).lseg;
+  return cdiv((s.B + (lseg ? s.N / lseg : 0)) * parts * s.H, 8) * 8 *
          cdiv((int64_t)(s.HV / s.H) * s.dv, kColsBlock);
 }
 
 template <typename T, int DK, int CH>
 hipError_t launch_scan(const SsmShape& s, const ScanArgs& a, hipStream_t st) {
-  const unsigned blocks = (unsigned)scan_blocks(s);
   if (a.lseg) {
-    hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, false>), dim3(blocks), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, false>),
+                       dim3((unsigned)scan_blocks(s, a.parts)), dim3(kThreads), 0, st, a);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     // enough workgroups to fill the device, few where many requests are likely not cut
     int parts = s.dv * s.dk / 1024;
     while (parts > 1 && s.B * s.HV * (parts / 2) >= 2048) parts /= 2;
-    hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)(s.B * s.HV * parts)), dim3(256), 0, st, a,
+    const auto join = a.parts == 1   ? ssm_join_kernel<1>
+                      : a.parts == 2 ? ssm_join_kernel<2>
+                                     : ssm_join_kernel<4>;
+    hipLaunchKernelGGL(join, dim3((unsigned)(s.B * s.HV * parts)), dim3(256), 0, st, a,
                        s.dv * s.dk, parts);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, true>), dim3(blocks), dim3(kThreads), 0, st, a);
+  hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, true>), dim3((unsigned)scan_blocks(s, 1)),
+                     dim3(kThreads), 0, st, a);
   return hipGetLastError();
 }
 
@@ -852,7 +937,7 @@ bool ssm_prefill_grids_fit(const SsmShape& s) {
   // the byte offsets inside a chunk's rows are 32-bit
   const int64_t row = (s.HV * (int64_t)s.dv > s.H * (int64_t)s.dk ? s.HV * (int64_t)s.dv
                                                                   : s.H * (int64_t)s.dk) * 4;
-  return row * 64 <= 0x7FFFFFFF && grid_ok(scan_blocks(s), kThreads) &&
+  return row * 64 <= 0x7FFFFFFF && grid_ok(scan_blocks(s, cut_of(s).parts), kThreads) &&
          (!short_tokens(s) || ssm_token_grid_fits(s)) && grid_ok(s.B * s.HV * (s.dv * s.dk / 1024), 256);
 }
 
@@ -861,11 +946,11 @@ hipError_t launch_ssm_prefill(const SsmShape& s, const void* C, const void* B, c
                               const float* D, float* state, const int64_t* idx,
                               const int64_t* cu, void* out, char* ws, hipStream_t st) {
   const ScanLayout L = scan_layout(s);
-  const int lseg = segment_tokens(s);
+  const Cut c = cut_of(s);
   ScanArgs a{C, B, x, dt, A_log, dt_bias, D, state, idx, cu, out, (float*)(ws + L.state),
              (float*)(ws + L.decay), s.N, s.B, s.pool, s.H, s.HV, s.dv, s.HV / s.H,
-             (int)cdiv((int64_t)(s.HV / s.H) * s.dv, kColsBlock), lseg,
-             (int)max_cut(s, lseg), short_tokens(s)};
+             (int)cdiv((int64_t)(s.HV / s.H) * s.dv, kColsBlock), c.lseg,
+             (int)max_cut(s, c.lseg), c.parts, short_tokens(s)};
   if (a.short_len)
     if (const hipError_t e = launch_ssm_short(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu,
                                               out, a.short_len, st);

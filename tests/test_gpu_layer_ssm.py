@@ -105,6 +105,30 @@ def test_ssm_one_long_request(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths,hv,dv", [([8960, 40], 256, 64), ([40, 15999], 64, 256)])
+def test_ssm_long_pieces(dtype, lengths, hv, dv):
+    """Pieces of thousands of tokens, whose states are formed in parts: heads that forget within a
+    few tokens beside heads that never do, in one workgroup where heads are narrow. Heads do not
+    mix, so the recurrence of a few of them is enough."""
+    from layer_util import DT
+    g = torch.Generator(device=DEV).manual_seed(len(lengths) + hv)
+    rn = lambda *s: torch.randn(*s, device=DEV, generator=g)  # noqa: E731
+    n, dk, heads = sum(lengths), 64, [0, 1, hv // 2, hv - 1]
+    a_log = torch.full((hv,), 4.0, device=DEV)
+    a_log[heads] = torch.tensor([-4.0, 4.6, 0.0, 2.0], device=DEV)
+    c = dict(C=(0.6 * rn(n, 1, dk)).to(DT[dtype]), B=(0.6 * rn(n, 1, dk)).to(DT[dtype]),
+             x=(0.8 * rn(n, hv, dv)).to(DT[dtype]), dt=rn(n, hv), A_log=a_log,
+             dt_bias=rn(hv) - 3, D=rn(hv), pool=0.3 * rn(2, hv, dv, dk), idx=np.array([1, 0]),
+             cu=np.concatenate([[0], np.cumsum(lengths)]).astype(int))
+    out, pool = call(c)
+    few = {k: c[k][:, heads] for k in ("x", "dt", "pool")}
+    few.update({k: c[k][heads] for k in ("A_log", "dt_bias", "D")}, C=c["C"], B=c["B"])
+    for k, v in few.items():
+        c[k], c[k + "64"] = v, np64(v)
+    check(c, dtype, out[:, heads], pool[:, heads], f"ssm {dtype} {lengths} HV={hv} dv={dv}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dt_mean,a_hi", [(3.0, 16.0), (30.0, 2.0), (-90.0, 16.0), (-12.0, 1.0)])
 def test_ssm_gates_at_their_ends(dtype, dt_mean, a_hi):
     """Decays that erase the state in one token, steps that vanish, decays next to one."""
