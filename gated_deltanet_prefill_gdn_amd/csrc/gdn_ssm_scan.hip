@@ -764,8 +764,15 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 }
 
 // The pieces' states (OUTPUT false); the outputs of pieces, and whole requests.
+// Workgroups of a CU that the registers are held to (fp32: LDS for one at dk >= 128): outputs keep
+// the next C, the scores and a bf16 state in them too, states alone leave room for three (8 ragged
+// requests, 64 heads of 64 x 128: 112 us, with two 136). At dk = 256 a compiler left free takes more
+// than half the registers, and one workgroup a CU: 16384 tokens, 8 heads of 256 x 256, 176 us
+// instead of 158, 10 ragged requests 462 instead of 273.
+template <typename T, int DK, bool OUTPUT>
+constexpr int kGroupsPerCU = sizeof(T) == 4 ? 1 : OUTPUT || DK == 256 ? 2 : 3;
 template <typename T, int DK, int CH, bool OUTPUT>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DK < 256 ? 2 : 1) void ssm_scan_kernel(ScanArgs a) {
+__global__ __launch_bounds__(kThreads, (kGroupsPerCU<T, DK, OUTPUT>)) void ssm_scan_kernel(ScanArgs a) {
   __shared__ __align__(16) char lds[OUTPUT ? Dims<T, DK, CH>::Bytes : Dims<T, DK, CH>::AtC];
   // Workgroups are dealt to the eight XCDs in turn: the column blocks of a (segment, group) go to
   // one of them, one after the other, and find B and C in its L2. The XCD of a group changes from
@@ -862,7 +869,7 @@ struct Cut {
 };
 Cut cut_of(const SsmShape& s) {
   const int64_t blocks = cdiv((int64_t)(s.HV / s.H) * s.dv, kColsBlock) * s.H;
-  const int64_t slots = s.dk < 256 ? 512 : 256;
+  constexpr int64_t slots = 512;
   int64_t best = 0, cost = INT64_MAX;
   for (int k = 1; k <= 4; ++k) {
     const int64_t pieces2 = 2 * k * slots / blocks - s.B;  // twice the pieces for N tokens
