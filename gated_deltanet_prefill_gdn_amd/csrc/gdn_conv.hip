@@ -9,7 +9,9 @@
 //
 // All three are bound by HBM: one pass over the token rows, a thread owning VEC channels (one
 // 16-byte vector) and a run of tokens whose window slides through registers, so every input row
-// is read once but for the W - 1 rows where runs meet.
+// is read once but for the W - 1 rows where runs meet. Measured, bf16, W = 4: 33860 tokens of 8192
+// channels 220 us (5.2 TB/s), 512 single tokens of 8192 channels 12.3 us (5.6 TB/s), gradients of
+// 16384 tokens of 6144 channels 167 us (5.0 TB/s) and 11 for the sums and the states' gradients.
 #include "gdn_layer.h"
 
 namespace gdn {
@@ -182,7 +184,9 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(
       }
       store_vec<VEC>(to, y);
     };
-    constexpr int U = 8;  // rows in flight
+    // Rows in flight, as they are stored: 33860 tokens of 8192 channels take 317 us with one row
+    // converted at its load, 231 with four kept in bf16, 221 with eight.
+    constexpr int U = 8;
     Raw<T, VEC> cur[U];
     for (; t + U <= run_end; t += U, xp += U * x_stride, op += U * ld) {
 #pragma unroll
@@ -452,8 +456,8 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_state_kernel(
   for (int i = 0; i < W - 1; ++i) dstate0[(req * (W - 1) + i) * (int64_t)ch + c] = du[i];
 }
 
-// Tokens of a tile: long enough that the window's rows are a small share of what a tile reads,
-// short enough that a small call still spreads over the device.
+// Tokens of a tile: long enough that the window's rows, which mostly hit in L2, are a small share
+// of what a tile reads, short enough that a small call still spreads over the device.
 int fwd_tile(const ConvShape& s, int vec) {
   const int64_t cols = cdiv(cdiv(s.ch, vec), kThreads);
   int tile = 32;

@@ -10,9 +10,12 @@
 //   gate first: dz = du x silu'(z),             dx = du silu(z).
 //
 // Bound by HBM: a row stays in the registers of TPR threads (NC vectors of VEC elements each)
-// from its one load to its store; the variance is taken of the centred row, in fp32. The
-// backward forms the row's statistics again from x, which it has to read anyway, so the forward
-// keeps nothing for it.
+// from its one load to its store; the variance is taken of the centred row, in fp32. The backward
+// forms the row's statistics again from x, which it has to read anyway, so the forward keeps
+// nothing for it. Measured: forward 33860 x 32 gated rows of 128, bf16, 155 us (5.4 TB/s);
+// gradients of 16384 x 16 such rows 61 us (5.5 TB/s) and 6 for the sums, of 16384 rows of 4096 87
+// us (4.9 TB/s) and 9. A short row takes 8 to 64 threads, so that all loads of a wave are one
+// vector a thread and the sums stay in a wave; longer ones a workgroup.
 #include "gdn_layer.h"
 
 namespace gdn {
@@ -369,9 +372,9 @@ int rows_per_block(const Pick& p) { return p.tpr > 256 ? 1 : 256 / p.tpr; }
 
 // Workgroups of a launch; the rest of the rows in the kernel's loop, which keeps the weights (and
 // the gradients' sums) in registers. Forward: the more the better (33860 x 32 rows of 128, gated:
-// 159 us with 16384, 168 with 4096; the next row's loads ahead of this row's work took 169). Backward:
-// each writes a partial row of dweight and dbias, and 768 are what the device holds (16384 rows of
-// 4096: 107 us with 768 and with 1024, 111 with 512; heads of 128: 69, 71 and 77).
+// 159 us with 16384, 168 with 4096; the next row's loads ahead of this row's work took 169).
+// Backward: each writes a partial row of dweight and dbias, and 768 are what the device holds
+// (16384 rows of 4096: 107 us with 768 and with 1024, 111 with 512; heads of 128: 69, 71 and 77).
 int64_t fwd_blocks(const NormShape& s, const Pick& p) {
   const int64_t all = cdiv(s.N * s.heads, rows_per_block(p));
   return all < 16384 ? all : 16384;
@@ -436,9 +439,11 @@ hipError_t bwd_k(const NormShape& s, int64_t blocks, const void* x, const float*
     case 102402: return F<T, VEC, 1024, 2>(__VA_ARGS__);              \
   }                                                                   \
   if constexpr (VEC < 8)                                              \
-    if (p.tpr == 1024 && p.nc == 4) return F<T, VEC, 1024, 4>(__VA_ARGS__);                                                                   \
+    if (p.tpr == 1024 && p.nc == 4)                                   \
+      return F<T, VEC, 1024, 4>(__VA_ARGS__);                         \
   if constexpr (VEC == 1)                                             \
-    if (p.tpr == 1024 && p.nc == 16) return F<T, VEC, 1024, 16>(__VA_ARGS__); \
+    if (p.tpr == 1024 && p.nc == 16)                                  \
+      return F<T, VEC, 1024, 16>(__VA_ARGS__);                        \
   return hipErrorInvalidValue
 
 template <typename T, int VEC>

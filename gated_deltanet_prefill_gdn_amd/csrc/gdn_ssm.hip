@@ -190,7 +190,8 @@ hipError_t launch_ssm_short(const SsmShape& s, const void* C, const void* B, con
                             const float* dt, const float* A_log, const float* dt_bias,
                             const float* D, float* state, const int64_t* idx, const int64_t* cu,
                             void* out, int64_t max_len, hipStream_t st) {
-  return launch_token_any<false>(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu, out, max_len, st);
+  return launch_token_any<false>(s, C, B, x, dt, A_log, dt_bias, D, state, idx, cu, out, max_len,
+                                 st);
 }
 
 }  // namespace layer
