@@ -84,14 +84,16 @@ def stage_bytes(p, s_qkv: int, s_ws: int, n_chunks: int):
 DECODE_SOURCES = ("gdn_decode.hip", "gdn_internal.h")
 PROMOTE_SOURCES = ("gdn_promote.hip", "gdn_internal.h", "gdn_mfma.h")
 BACKWARD_SOURCES = ("gdn_backward.hip", "gdn_backward.h", "gdn_internal.h", "gdn_plan_gate.hip")
+LAYER_SOURCES = ("gdn_layer.h", "gdn_layer_api.hip", "gdn_conv.hip", "gdn_norm.hip",
+                 "gdn_ssm.hip", "gdn_ssm_scan.hip")
 PREFILL_F32_SOURCES = ("gdn_ref.hip", "gdn_plan_gate.hip", "gdn_api.hip", "gdn_internal.h",
                        "gdn_mfma.h")
 
 
 def kernel_source_hash(kind: str = "prefill") -> str:
     """sha256[:16] over the kernel sources a measurement depends on: for "prefill" (the
-    bf16 path) every .hip / .h file of csrc except the decode, Promote, backward and fp32
-    kernels' own files, for "prefill_f32" PREFILL_F32_SOURCES, for "decode" DECODE_SOURCES,
+    bf16 path) every .hip / .h file of csrc except the decode, Promote, backward, fp32 and
+    layer kernels' own files, for "prefill_f32" PREFILL_F32_SOURCES, for "decode" DECODE_SOURCES,
     for "promote" PROMOTE_SOURCES, for "backward" BACKWARD_SOURCES."""
     csrc = os.path.join(ROOT, "gated_deltanet_prefill_gdn_amd", "csrc")
     if kind == "decode":
@@ -105,7 +107,7 @@ def kernel_source_hash(kind: str = "prefill") -> str:
     else:
         files = sorted(f for f in os.listdir(csrc) if f.endswith((".hip", ".h"))
                        and f not in ("gdn_decode.hip", "gdn_promote.hip", "gdn_backward.hip",
-                                     "gdn_backward.h", "gdn_ref.hip"))
+                                     "gdn_backward.h", "gdn_ref.hip", *LAYER_SOURCES))
     h = hashlib.sha256()
     for f in files:
         h.update(f.encode())

@@ -295,3 +295,14 @@ def test_norm_backward_binding_refusals():
                     (dict(z=z(6, 2, 64), dz=z(6, 2, 64, dtype=F32)), TypeError)):
         with pytest.raises(err):
             gdn.gdn_norm_bwd(**{**a, **kw})
+
+
+def test_prefill_measurements_do_not_depend_on_the_layer_sources():
+    """The stored counters of the prefill stay valid when a layer kernel changes."""
+    import os
+
+    import bench
+    csrc = os.path.join(os.path.dirname(gdn.__file__), "csrc")
+    own = {f for f in os.listdir(csrc)
+           if f.startswith(("gdn_layer", "gdn_conv", "gdn_norm", "gdn_ssm"))}
+    assert set(bench.LAYER_SOURCES) == own
