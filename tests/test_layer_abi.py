@@ -299,8 +299,6 @@ def test_norm_backward_binding_refusals():
 
 def test_prefill_measurements_do_not_depend_on_the_layer_sources():
     """The stored counters of the prefill stay valid when a layer kernel changes."""
-    import os
-
     import bench
     csrc = os.path.join(os.path.dirname(gdn.__file__), "csrc")
     own = {f for f in os.listdir(csrc)
