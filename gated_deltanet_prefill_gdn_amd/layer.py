@@ -147,6 +147,10 @@ def _index(t, name, like):
     return t.shape[0]
 
 
+def _slots(pool):
+    return pool.shape[0] if pool.dim() else 0
+
+
 def _requests(cache_indices, cu_seqlens, like):
     """B; cache_indices may be None (a convolution without a state pool)."""
     n = None if cache_indices is None else _index(cache_indices, "cache_indices", like)
@@ -166,7 +170,8 @@ def conv_problem(x, width, dims, batch, pool_size=0, silu=True, dout_dtype=GDN_D
     if not 1 <= len(dims) <= 3:
         raise ValueError("one to three outputs")
     ch = sum(dims)
-    stride = _rows(x, "x", (ch,), x)
+    dense = x.is_contiguous() and x.dim() == 2 and x.shape[1] == ch
+    stride = ch if dense else _rows(x, "x", (ch,), x)
     return GdnConvProblem(x.shape[0], batch, pool_size, stride,
                           ch if dx_stride is None else dx_stride,
                           _Three(*dims), width, _code(x, "x"),
@@ -192,7 +197,7 @@ def _conv_check(x, weight, bias, state_pool, cache_indices, cu_seqlens, dims, si
     if state_pool is not None:
         if cache_indices is None:
             raise ValueError("cache_indices are required with a state_pool")
-        _shape(state_pool, "state_pool", state_pool.shape[:1] + (w - 1, ch), x.dtype, x)
+        _shape(state_pool, "state_pool", (_slots(state_pool), w - 1, ch), x.dtype, x)
     batch = _requests(cache_indices if state_pool is not None else None, cu_seqlens, x)
     prob = conv_problem(x, w, dims, batch, 0 if state_pool is None else state_pool.shape[0], silu,
                         **kw)
@@ -204,8 +209,12 @@ def _conv_outs(outs, x, dims, stream):
     if outs is None:
         if len(dims) == 1:
             return (_like(stream, x),)
-        dtype, dev = x.dtype, x.device
-        return tuple([_new(stream, (n, d), dtype, dev) for d in dims])
+        if stream is not None:
+            return tuple([_new(stream, (n, d), x.dtype, x.device) for d in dims])
+        made = [x.new_empty((n, dims[0]))]
+        for d, before in zip(dims[1:], dims):
+            made.append(torch.empty_like(made[-1]) if d == before else x.new_empty((n, d)))
+        return tuple(made)
     if len(outs) != len(dims):
         raise ValueError(f"{len(dims)} outputs are wanted, got {len(outs)}")
     for i, (o, d) in enumerate(zip(outs, dims)):
@@ -313,7 +322,7 @@ def _ssm_check(C, B, x, dt, A_log, dt_bias, D, state_pool, cache_indices, cu_seq
     _shape(dt_bias, "dt_bias", (hv,), _F32, x)
     if D is not None:
         _shape(D, "D", (hv,), _F32, x)
-    _shape(state_pool, "state_pool", state_pool.shape[:1] + (hv, dv, dk), _F32, x)
+    _shape(state_pool, "state_pool", (_slots(state_pool), hv, dv, dk), _F32, x)
     batch = _requests(cache_indices, cu_seqlens, x)
     if cu_seqlens is None and batch != n:
         raise ValueError("cache_indices must have one entry per row of x")
@@ -359,7 +368,7 @@ def gdn_ssm_decode_fwd(C, B, x, dt, A_log, dt_bias, D, state_pool, cache_indices
 def norm_problem(x, z=None, eps=1e-6, rms=True, gate_first=False, dz=None) -> GdnNormProblem:
     """Descriptor of a norm of x [N, heads, dim] (see gdn_norm_problem_t)."""
     inner = x.shape[1:]
-    xs = _rows(x, "x", inner, x)
+    xs = inner.numel() if x.is_contiguous() else _rows(x, "x", inner, x)
     zs = 0 if z is None else _rows(z, "z", inner, x)
     dzs = zs if dz is None else _rows(dz, "dz", inner, x)
     return GdnNormProblem(x.shape[0], xs, zs, dzs, inner[0], inner[1], _code(x, "x"),
