@@ -927,15 +927,21 @@ int64_t scan_blocks(const SsmShape& s, int parts) {
          cdiv((int64_t)(s.HV / s.H) * s.dv, kColsBlock);
 }
 
+// Workgroups of a state in the join: enough to fill the device, few where many requests are likely
+// not cut.
+int join_parts(const SsmShape& s) {
+  int parts = s.dv * s.dk / 1024;
+  while (parts > 1 && s.B * s.HV * (parts / 2) >= 2048) parts /= 2;
+  return parts;
+}
+
 template <typename T, int DK, int CH>
 hipError_t launch_scan(const SsmShape& s, const ScanArgs& a, hipStream_t st) {
   if (a.lseg) {
     hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, false>),
                        dim3((unsigned)scan_blocks(s, a.parts)), dim3(kThreads), 0, st, a);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    // enough workgroups to fill the device, few where many requests are likely not cut
-    int parts = s.dv * s.dk / 1024;
-    while (parts > 1 && s.B * s.HV * (parts / 2) >= 2048) parts /= 2;
+    const int parts = join_parts(s);
     const auto join = a.parts == 1   ? ssm_join_kernel<1>
                       : a.parts == 2 ? ssm_join_kernel<2>
                                      : ssm_join_kernel<4>;
@@ -958,7 +964,7 @@ bool ssm_prefill_grids_fit(const SsmShape& s) {
                                                                   : s.H * (int64_t)s.dk) * 4;
   return row * 64 <= 0x7FFFFFFF && grid_ok(scan_blocks(s, cut_of(s).parts), kThreads) &&
          (!short_tokens(s) || ssm_token_grid_fits(s)) &&
-         grid_ok(s.B * s.HV * (s.dv * s.dk / 1024), 256);
+         (!cut_of(s).lseg || grid_ok(s.B * s.HV * join_parts(s), 256));
 }
 
 hipError_t launch_ssm_prefill(const SsmShape& s, const void* C, const void* B, const void* x,
