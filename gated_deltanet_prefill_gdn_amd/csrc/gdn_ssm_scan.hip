@@ -23,13 +23,15 @@
 // so long pieces are taken in parts, which spread the slow heads over the device.
 //
 // Precision: bf16 inputs enter the products as they are. The decayed x of the state's update are
-// three bf16 (24 bits), since states are fp32 results; the decayed scores and the state that S C
-// reads are one bf16 each (2^-8 of a term: the output is rounded by as much), and so are the
-// decayed x where a piece's state is only formed to be read so. For fp32 inputs every operand is
-// three bf16 (24 bits) and a product takes the six pairs of parts that reach 2^-24: 2.7 times the
-// rate of the fp32 matrix instructions. Gates and their sums are fp32 (the sums of fp32 inputs
-// fp64), and exponents are only taken of differences that are not positive, so strong decays
-// underflow to zero and nothing overflows.
+// three bf16 (24 bits), since states are fp32 results. What only outputs take, which end as bf16, is
+// two bf16 (16 bits): the decayed scores, the state that S C reads, and the decayed x where a piece's
+// state is only formed to be read so. One bf16 each would be a rounding as large as the output's own
+// (errors of 1.79e-3 of the outputs' size instead of 1.66e-3, twelve times a rounding where terms
+// cancel; 131072 tokens take 945 us instead of 1100). For fp32 inputs every operand is three bf16 and
+// a product takes the six pairs of parts that reach 2^-24: 2.7 times the rate of the fp32 matrix
+// instructions. Gates and their sums are fp32 (fp32 inputs: G of a chunk's outputs in fp64), and
+// exponents are only taken of differences that are not positive, so strong decays underflow to zero
+// and nothing overflows.
 //
 // Measured, bf16: 131072 tokens, 32 heads of 128 x 128, 964 us (762 us of them outputs, 5.1 TB/s of
 // what they move: bound by bytes); 8 ragged requests of 33860 tokens, 64 heads of 64 x 128 that
@@ -54,7 +56,6 @@ typedef mfma::f32x4 acc4;
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kColsWave = 32, kColsBlock = kColsWave * kWaves;  // value columns
-constexpr int kHeads = kColsBlock / 64;  // heads of a workgroup at most
 
 struct ScanArgs {
   const void *C, *B, *x;
@@ -235,7 +236,9 @@ struct Gates {
   float eG[CH];        // e^G
   float row[CH];       // e^{G_t - G at the start of t's tile}
   float w[CH];         // d e^{G_n - G}: weight in the state's update
-  float col[CH / 16 - 1][CH];  // [tile - 1]: d_j e^{G at the tile's start - G_j}, j before it
+  // d_j e^{G at tile k's start - G_j} for the tokens j before it, k = 1, 2, ..: 16 k from at(k) on
+  float col[CH / 16 * (CH / 16 - 1) / 2 * 16];
+  static __device__ __forceinline__ int at(int k) { return 8 * k * (k - 1); }
   float total[4];              // G_n (its own 16 bytes)
 };
 
@@ -331,9 +334,11 @@ __device__ __forceinline__ bool deal(int wave, int i, int& tt, int& jt) {
 // piece from zero; the outputs of a piece from its start state.
 enum Mode { kWhole, kState, kOutput };
 
-template <typename T, int DK, int CH>
+// HEADS: heads of a workgroup at most, two where a head has 64 columns.
+template <typename T, int DK, int CH, int HEADS>
 struct Dims {
-  static constexpr int NP = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of an input, scores and S in S C
+  static constexpr int NP = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of an input
+  static constexpr int PS = sizeof(T) == 4 ? 3 : 2;  // ... of the decayed scores and of S in S C
   // LDS rows. C is read in 8-byte pieces down 16 rows: 4.5 cycles for a wave's read where the
   // stride is 2 mod 4 words, 8 or 16 elsewhere. B and x are read transposed and in 16-byte pieces:
   // no conflicts and 4.9 cycles where it is 8 mod 16 words, 8 elsewhere (measured).
@@ -341,24 +346,28 @@ struct Dims {
   static constexpr int TileC = CH * LDC, TileB = CH * LDB, TileX = CH * LDX, TileP = CH * LDP;
   using R = typename std::conditional<sizeof(T) == 4, double, float>::type;
   using G = Gates<CH, R>;
-  // LDS: B, x, four gate sets; with outputs also C and the decayed scores of up to two heads
+  // LDS: B, x, four gate sets; with outputs also C and the heads' decayed scores. For bf16 inputs
+  // those of two heads start in C's place, which has been read by then: two workgroups a CU have
+  // 80 KB each.
+  static constexpr bool Over = sizeof(T) == 2 && HEADS == 2;
   static constexpr int AtX = NP * TileB * 2, AtG = AtX + NP * TileX * 2;
-  static constexpr int AtC = AtG + kWaves * (int)sizeof(G), AtP = AtC + NP * TileC * 2;
-  static constexpr int Bytes = AtP + kHeads * NP * TileP * 2;
+  static constexpr int AtC = AtG + kWaves * (int)sizeof(G), EndC = AtC + NP * TileC * 2;
+  static constexpr int AtP = Over ? AtC : EndC, EndP = AtP + HEADS * PS * TileP * 2;
+  static constexpr int Bytes = EndP > EndC ? EndP : EndC;
   static_assert(AtX % 16 == 0 && AtG % 16 == 0 && AtC % 16 == 0 && AtP % 16 == 0, "16-byte rows");
 };
 
 // A piece's state: sg is the part of the piece, `ws` its place and `end` the piece's end.
-template <typename T, int DK, int CH, Mode MODE>
+template <typename T, int DK, int CH, int HEADS, Mode MODE>
 __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& sg, int in_seg,
                                              char* lds, int64_t ws = 0, int64_t end = 0) {
-  using D = Dims<T, DK, CH>;
+  using D = Dims<T, DK, CH, HEADS>;
   using R = typename D::R;
   using G = typename D::G;
   constexpr bool F32 = sizeof(T) == 4, OUT = MODE != kState;
-  constexpr int NP = D::NP;
+  constexpr int NP = D::NP, PS = D::PS;
   // ... of the update's decayed x: the state of a piece's outputs is only read by S C
-  constexpr int NU = !F32 && MODE == kOutput ? 1 : 3;
+  constexpr int NU = MODE == kOutput ? PS : 3;
   constexpr int NT = CH / 16, NK = CH / 32;      // token tiles, k steps over tokens
   constexpr int NS = DK / 16, NKS = DK / 32;     // state tiles, k steps over state entries
   constexpr int TRI = NT == 4 ? 3 : 1;           // tiles of scores for a wave at most
@@ -368,8 +377,6 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
   __bf16* const s_x = reinterpret_cast<__bf16*>(lds + D::AtX);
   G* const s_g = reinterpret_cast<G*>(lds + D::AtG);
   __bf16* const s_c = reinterpret_cast<__bf16*>(lds + D::AtC);
-  // decayed scores, row t; entry 32 k + 8 g + e is token j = 32 k + kperm(g, e)
-  __bf16* const s_p = reinterpret_cast<__bf16*>(lds + D::AtP);
 
   const int h = in_seg / a.blocks_per_group;
   const int col0 = in_seg % a.blocks_per_group * kColsBlock;  // of the group's columns
@@ -385,9 +392,11 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
   // Heads of the workgroup, and the one this wave's columns belong to. The four gate sets hold
   // four chunks of one head or two of two: each wave forms one set, of head gh and the chunk
   // gc after the batch's first.
-  const int hv0 = h * a.rep + col0 / a.dv, nh = (ncols + a.dv - 1) / a.dv;
+  const int hv0 = h * a.rep + col0 / a.dv, nh = HEADS == 1 ? 1 : (ncols + a.dv - 1) / a.dv;
   const int batch = nh == 2 ? 2 : 4, gh = nh == 2 ? wv >> 1 : 0, gc = nh == 2 ? wv & 1 : wv;
   const int hw = nh == 2 ? kColsWave * wv / a.dv : 0;
+  // decayed scores, row t; entry 32 k + 8 g + e is token j = 32 k + kperm(g, e)
+  __bf16* const s_p = reinterpret_cast<__bf16*>(lds + D::AtP);
   auto gate_set = [&](int head, int chunk) -> G& {
     return s_g[nh == 2 ? 2 * head + (chunk & 1) : chunk & 3];
   };
@@ -417,14 +426,14 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
   const float decay = -expf(a.A_log[hv0 + gh]) * kLog2e, dtb = a.dt_bias[hv0 + gh];
   const float dskip = a.D ? a.D[hv] : 0.f;
   // a piece's state: sum of g from the chunks walked to the piece's end, of each head
-  float behind[kHeads] = {};
+  float behind[HEADS] = {};
   if constexpr (MODE == kState) {
     float* const s_sum = reinterpret_cast<float*>(lds);
     bool more = sg.t0 < sg.t1;
     for (int64_t t = sg.t1; more && t < end; t += 4 * kThreads) {
-      float sum[kHeads] = {};
+      float sum[HEADS] = {};
 #pragma unroll
-      for (int hh = 0; hh < kHeads; ++hh) {
+      for (int hh = 0; hh < HEADS; ++hh) {
         if (hh >= nh) break;
         const float rate = -expf(a.A_log[hv0 + hh]) * kLog2e, shift = a.dt_bias[hv0 + hh];
 #pragma unroll
@@ -439,7 +448,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
       __syncthreads();
       more = false;
 #pragma unroll
-      for (int hh = 0; hh < kHeads; ++hh)
+      for (int hh = 0; hh < HEADS; ++hh)
         if (hh < nh) {
 #pragma unroll
           for (int k = 0; k < kWaves; ++k) behind[hh] += s_sum[hh * kWaves + k];
@@ -480,10 +489,6 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
   };
   fetch(place(0));
   fetch_dt(0);
-  if constexpr (OUT) {  // scores above the diagonal stay zero
-    for (int i = tid; i < kHeads * NP * kTileP / 8; i += kThreads)
-      reinterpret_cast<u32x4*>(s_p)[i] = u32x4{0, 0, 0, 0};
-  }
 
   for (int chunk = 0; chunk < chunks; ++chunk) {
     const int64_t t0 = place(chunk);
@@ -526,7 +531,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
           gt.row[lane] = exp2_((float)local);
 #pragma unroll
           for (int k = 1; k < NT; ++k)
-            gt.col[k - 1][lane] = lane < 16 * k ? step * exp2_((float)(at[k] - Gp)) : 0.f;
+            if (lane < 16 * k) gt.col[G::at(k) + lane] = step * exp2_((float)(at[k] - Gp));
         }
         gt.w[lane] = step * exp2_(row_behind(gl) + after);
       }
@@ -537,17 +542,9 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
     if (chunk + 1 < chunks) fetch(place(chunk + 1));
     const G& gt = gate_set(hw, chunk);
 
-    bfrag xf[NP][2][NK];  // x, column p0 + 16 pt + r, tokens 32 k + kperm
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-#pragma unroll
-      for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-        for (int k = 0; k < NK; ++k)
-          xf[p][pt][k] = frag_col(s_x + p * kTileX, LDX, kColsWave * wv + 16 * pt, k, g, r);
-
+    acc4 y[NT][2];  // Y^T: columns 16 pt + 4 g .. + 3 of token 16 t + r
+    acc4 sc[TRI];   // scores^T, j x t: each wave some of the tiles
     if constexpr (OUT) {
-      // scores^T, j x t: each wave some of the tiles, decayed for each of the workgroup's heads
 #pragma unroll
       for (int i = 0; i < TRI; ++i) {
         int tt, jt;
@@ -567,130 +564,156 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
                                                            (16 * jt + r) * LDB + 32 * k + 8 * g),
                            c, half[k % 2]);
           }
-        const acc4 sc = half[0] + half[1];
-        for (int hh = 0; hh < nh; ++hh) {
-          const G& gs = gate_set(hh, chunk);
-          float v[4];
-          if (jt < tt) {
-            const acc4 c = *reinterpret_cast<const acc4*>(&gs.col[tt - 1][16 * jt + 4 * g]);
-            const float row = gs.row[16 * tt + r];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = sc[e] * (c[e] * row);
-          } else {
-            const acc4 d = *reinterpret_cast<const acc4*>(&gs.step[16 * jt + 4 * g]);
-            const R Gt = gs.G[16 * tt + r];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float ex = exp2_((float)(Gt - gs.G[16 * jt + 4 * g + e])) * d[e];
-              v[e] = 4 * g + e <= r ? sc[e] * ex : 0.f;
-            }
-          }
-          uint32_t lo[NP], hi[NP];
-          split<NP>(v[0], v[1], lo);
-          split<NP>(v[2], v[3], hi);
-#pragma unroll
-          for (int p = 0; p < NP; ++p)
-            *reinterpret_cast<u32x2*>(s_p + (hh * NP + p) * kTileP + (16 * tt + r) * LDP +
-                                      32 * (jt / 2) + 8 * g + 4 * (jt % 2)) = u32x2{lo[p], hi[p]};
-        }
+        sc[i] = half[0] + half[1];
       }
-      // S^T as the operand of S C: formed once for the chunk's token tiles, or, where there are
-      // but two of them, in their loop
-      auto state_operand = [&](int k, bfrag (&sb)[NP][2]) {
+      // the scores, decayed for each of the workgroup's heads
+      auto decay_scores = [&]() {
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt) {
-          u32x4 words[NP];
+        for (int i = 0; i < TRI; ++i) {
+          int tt, jt;
+          if (!deal<NT>(wv, i, tt, jt)) break;
+          for (int hh = 0; hh < HEADS; ++hh) {
+            if (hh >= nh) break;
+            const G& gs = gate_set(hh, chunk);
+            __bf16* const to = s_p + hh * PS * kTileP + (16 * tt + r) * LDP + 32 * (jt / 2) + 8 * g +
+                               4 * (jt % 2);
+            float v[4];
+            if (jt < tt) {
+              const acc4 c = *reinterpret_cast<const acc4*>(&gs.col[G::at(tt) + 16 * jt + 4 * g]);
+              const float row = gs.row[16 * tt + r];
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            uint32_t part[NP];
-            const acc4 v = st[2 * k + e / 4][pt];
-            split<NP>(v[e % 4], v[e % 4 + 1], part);
+              for (int e = 0; e < 4; ++e) v[e] = sc[i][e] * (c[e] * row);
+            } else {
+              const acc4 d = *reinterpret_cast<const acc4*>(&gs.step[16 * jt + 4 * g]);
+              const R Gt = gs.G[16 * tt + r];
+              R Gj[4];
 #pragma unroll
-            for (int p = 0; p < NP; ++p) words[p][e / 2] = part[p];
+              for (int e = 0; e < 4; ++e) Gj[e] = gs.G[16 * jt + 4 * g + e];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float ex = sc[i][e] * (exp2_((float)(Gt - Gj[e])) * d[e]);
+                asm volatile("" : "+v"(ex));  // no branch around each entry
+                v[e] = 4 * g + e <= r ? ex : 0.f;
+              }
+              if (jt % 2 == 0)  // the tile beside it shares its k step
+#pragma unroll
+                for (int p = 0; p < PS; ++p)
+                  *reinterpret_cast<u32x2*>(to + p * kTileP + 4) = u32x2{0, 0};
+            }
+            uint32_t lo[PS], hi[PS];
+            split<PS>(v[0], v[1], lo);
+            split<PS>(v[2], v[3], hi);
+#pragma unroll
+            for (int p = 0; p < PS; ++p)
+              *reinterpret_cast<u32x2*>(to + p * kTileP) = u32x2{lo[p], hi[p]};
           }
-#pragma unroll
-          for (int p = 0; p < NP; ++p) sb[p][pt] = bf16x8_from_u32x4(words[p]);
         }
       };
-      bfrag sbs[NK > 1 ? NKS : 1][NP][2];
-      if constexpr (NK > 1) {
+      if constexpr (!D::Over) decay_scores();
+      // S C, and its decay
 #pragma unroll
-        for (int k = 0; k < NKS; ++k) state_operand(k, sbs[k]);
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt) y[t][pt] = acc4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < NKS; ++k) {
+        bfrag cf[NT][NP];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int p = 0; p < NP; ++p)
+            cf[t][p] = frag_kperm(s_c + p * kTileC + (16 * t + r) * LDC + 32 * k, g);
+        // (reads left among the products wait one by one: 131072 tokens 930 us instead of 894)
+        if constexpr (!F32) __builtin_amdgcn_sched_barrier(0);
+        bfrag sb[PS][2];
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt) {
+          u32x4 words[PS];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            uint32_t part[PS];
+            const acc4 v = st[2 * k + e / 4][pt];
+            split<PS>(v[e % 4], v[e % 4 + 1], part);
+#pragma unroll
+            for (int p = 0; p < PS; ++p) words[p][e / 2] = part[p];
+          }
+#pragma unroll
+          for (int p = 0; p < PS; ++p) sb[p][pt] = bf16x8_from_u32x4(words[p]);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            const bfrag c = cf[t][p];
+#pragma unroll
+            for (int q = 0; q + p < PS; ++q)
+#pragma unroll
+              for (int pt = 0; pt < 2; ++pt) y[t][pt] = mma_bf16(sb[q][pt], c, y[t][pt]);
+          }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float e = gt.eG[16 * t + r];
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt) y[t][pt] *= e;
+      }
+      if constexpr (D::Over) {
+        __syncthreads();  // C has been read
+        decay_scores();
       }
       __syncthreads();
-      // Y^T, two token tiles at a time: columns 16 pt + 4 g .. + 3 of token 16 t + r
-      const rsrc_t qo = chunk_rows(gout + t0 * ldx, ldx * (int)sizeof(T), rows,
-                                   kColsWave * (int)sizeof(T));
-      const __bf16* const ph = s_p + hw * NP * kTileP;
-#pragma unroll 1
-      for (int tp = 0; tp < NK; ++tp) {
-        acc4 yc[2][2], yp[2][2];  // of S C (without its decay), of scores times x
+    }
+    bfrag xf[NP][2][NK];  // x, column p0 + 16 pt + r, tokens 32 k + kperm
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+    for (int p = 0; p < NP; ++p)
 #pragma unroll
-          for (int pt = 0; pt < 2; ++pt) yc[u][pt] = yp[u][pt] = acc4{0.f, 0.f, 0.f, 0.f};
+      for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
-        for (int k = 0; k < NKS; ++k) {
-          bfrag(&sb)[NP][2] = sbs[NK > 1 ? k : 0];
-          if constexpr (NK == 1) state_operand(k, sb);
+        for (int k = 0; k < NK; ++k)
+          xf[p][pt][k] = frag_col(s_x + p * kTileX, LDX, kColsWave * wv + 16 * pt, k, g, r);
+
+    if constexpr (OUT) {
+      // + scores times x
+      const rsrc_t qo = chunk_rows(gout + t0 * ldx, ldx * (int)sizeof(T), live ? rows : 1,
+                                   live ? kColsWave * (int)sizeof(T) : 0);
+      const __bf16* const ph = s_p + hw * PS * kTileP;
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+      for (int t = 0; t < NT; ++t) {
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-              const bfrag c =
-                  frag_kperm(s_c + p * kTileC + (16 * (2 * tp + u) + r) * LDC + 32 * k, g);
+        for (int k = 0; k <= t / 2; ++k)
 #pragma unroll
-              for (int pt = 0; pt < 2; ++pt)
+          for (int q = 0; q < PS; ++q) {
+            const bfrag pf = *reinterpret_cast<const bfrag*>(ph + q * kTileP + (16 * t + r) * LDP +
+                                                             32 * k + 8 * g);
 #pragma unroll
-                for (int q = 0; q + p < NP; ++q) yc[u][pt] = mma_bf16(sb[q][pt], c, yc[u][pt]);
-            }
-        }
+            for (int p = 0; p < NP && p + q < PS; ++p)
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          if (k > tp) break;
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int q = 0; q < NP; ++q) {
-              const bfrag pf = *reinterpret_cast<const bfrag*>(
-                  ph + q * kTileP + (16 * (2 * tp + u) + r) * LDP + 32 * k + 8 * g);
-#pragma unroll
-              for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-                for (int p = 0; p + q < NP; ++p) yp[u][pt] = mma_bf16(xf[p][pt][k], pf, yp[u][pt]);
-            }
-        }
+              for (int pt = 0; pt < 2; ++pt) y[t][pt] = mma_bf16(xf[p][pt][k], pf, y[t][pt]);
+          }
         // + D x, and out: four columns of one token per lane
-        if (live) {
+        const int row = 16 * t + r;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int row = 16 * (2 * tp + u) + r;
-            const float e = gt.eG[row];
+        for (int pt = 0; pt < 2; ++pt) {
+          const int at = row * LDX + kColsWave * wv + 16 * pt + 4 * g;
+          float xv[4], o[4];
 #pragma unroll
-            for (int pt = 0; pt < 2; ++pt) {
-              const int at = row * LDX + kColsWave * wv + 16 * pt + 4 * g;
-              float xv[4], o[4];
+          for (int p = NP - 1; p >= 0; --p) {
+            const bf16x4 xp = *reinterpret_cast<const bf16x4*>(s_x + p * kTileX + at);
 #pragma unroll
-              for (int p = NP - 1; p >= 0; --p) {
-                const bf16x4 xp = *reinterpret_cast<const bf16x4*>(s_x + p * kTileX + at);
+            for (int i = 0; i < 4; ++i)
+              xv[i] = p == NP - 1 ? (float)xp[i] : xv[i] + (float)xp[i];
+          }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  xv[i] = p == NP - 1 ? (float)xp[i] : xv[i] + (float)xp[i];
-              }
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                o[i] = __builtin_fmaf(e, yc[u][pt][i], __builtin_fmaf(dskip, xv[i], yp[u][pt][i]));
-              const int to = row * (int)(ldx * sizeof(T)) + (16 * pt + 4 * g) * (int)sizeof(T);
-              if constexpr (F32) {
-                __builtin_amdgcn_raw_buffer_store_b128(
-                    __builtin_bit_cast(u32x4, f32x4{o[0], o[1], o[2], o[3]}), qo, to, 0, 0);
-              } else {
-                __builtin_amdgcn_raw_buffer_store_b64(
-                    __builtin_bit_cast(u32x2, bf16x4{(__bf16)o[0], (__bf16)o[1], (__bf16)o[2],
-                                                     (__bf16)o[3]}),
-                    qo, to, 0, 0);
-              }
-            }
+          for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(dskip, xv[i], y[t][pt][i]);
+          const int to = row * (int)(ldx * sizeof(T)) + (16 * pt + 4 * g) * (int)sizeof(T);
+          if constexpr (F32) {
+            __builtin_amdgcn_raw_buffer_store_b128(
+                __builtin_bit_cast(u32x4, f32x4{o[0], o[1], o[2], o[3]}), qo, to, 0, 0);
+          } else {
+            __builtin_amdgcn_raw_buffer_store_b64(
+                __builtin_bit_cast(u32x2, bf16x4{(__bf16)o[0], (__bf16)o[1], (__bf16)o[2],
+                                                 (__bf16)o[3]}),
+                qo, to, 0, 0);
           }
         }
       }
@@ -753,7 +776,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
     if constexpr (!OUT) {
       bool more = false;
 #pragma unroll
-      for (int hh = 0; hh < kHeads; ++hh)
+      for (int hh = 0; hh < HEADS; ++hh)
         if (hh < nh) {
           behind[hh] += gate_set(hh, chunk).total[0];
           more = more || !(exp2_(behind[hh]) == 0.f);
@@ -782,10 +805,11 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 // 176 us instead of 158, 10 ragged requests 462 instead of 273.
 template <typename T, int DK, bool OUTPUT>
 constexpr int kGroupsPerCU = sizeof(T) == 4 ? 1 : OUTPUT || DK == 256 ? 2 : 3;
-template <typename T, int DK, int CH, bool OUTPUT>
+template <typename T, int DK, int CH, int HEADS, bool OUTPUT>
 __global__ __launch_bounds__(kThreads, (kGroupsPerCU<T, DK, OUTPUT>)) void ssm_scan_kernel(
     ScanArgs a) {
-  __shared__ __align__(16) char lds[OUTPUT ? Dims<T, DK, CH>::Bytes : Dims<T, DK, CH>::AtC];
+  using D = Dims<T, DK, CH, HEADS>;
+  __shared__ __align__(16) char lds[OUTPUT ? D::Bytes : D::AtC];
   // Workgroups are dealt to the eight XCDs in turn: the column blocks of a (segment, group) go to
   // one of them, one after the other, and find B and C in its L2. The XCD of a group changes from
   // segment to segment, since groups differ in how far a piece's state reaches back.
@@ -798,16 +822,16 @@ __global__ __launch_bounds__(kThreads, (kGroupsPerCU<T, DK, OUTPUT>)) void ssm_s
   if (!find_segment(a, seg, sg)) return;
   if constexpr (OUTPUT) {
     if (sg.count > 1)
-      scan_segment<T, DK, CH, kOutput>(a, sg, in_seg, lds);
+      scan_segment<T, DK, CH, HEADS, kOutput>(a, sg, in_seg, lds);
     else
-      scan_segment<T, DK, CH, kWhole>(a, sg, in_seg, lds);
+      scan_segment<T, DK, CH, HEADS, kWhole>(a, sg, in_seg, lds);
   } else if (sg.count > 1) {
     const int part = unit / a.H % parts;
     const int len = ((int)(sg.t1 - sg.t0) + 64 * parts - 1) / (64 * parts) * 64;
     const int64_t end = sg.t1;
     sg.t0 += (int64_t)part * len;
     sg.t1 = sg.t0 + len < end ? sg.t0 + len : end;
-    scan_segment<T, DK, CH, kState>(a, sg, in_seg, lds, (int64_t)sg.ws * parts + part, end);
+    scan_segment<T, DK, CH, HEADS, kState>(a, sg, in_seg, lds, (int64_t)sg.ws * parts + part, end);
   }
 }
 
@@ -935,10 +959,10 @@ int join_parts(const SsmShape& s) {
   return parts;
 }
 
-template <typename T, int DK, int CH>
+template <typename T, int DK, int CH, int HEADS>
 hipError_t launch_scan(const SsmShape& s, const ScanArgs& a, hipStream_t st) {
   if (a.lseg) {
-    hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, false>),
+    hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, HEADS, false>),
                        dim3((unsigned)scan_blocks(s, a.parts)), dim3(kThreads), 0, st, a);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int parts = join_parts(s);
@@ -949,7 +973,7 @@ hipError_t launch_scan(const SsmShape& s, const ScanArgs& a, hipStream_t st) {
                        s.dv * s.dk, parts);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, true>), dim3((unsigned)scan_blocks(s, 1)),
+  hipLaunchKernelGGL((ssm_scan_kernel<T, DK, CH, HEADS, true>), dim3((unsigned)scan_blocks(s, 1)),
                      dim3(kThreads), 0, st, a);
   return hipGetLastError();
 }
@@ -982,9 +1006,14 @@ hipError_t launch_ssm_prefill(const SsmShape& s, const void* C, const void* B, c
                                               out, a.short_len, st);
         e != hipSuccess)
       return e;
-#define GDN_SCAN_CASE(DK, CHB)                                        \
-  if (s.dk == DK)                                                     \
-    return s.bf16 ? launch_scan<__bf16, DK, CHB>(s, a, st) : launch_scan<float, DK, 32>(s, a, st);
+#define GDN_SCAN_CASE(DK, CHB)                                          \
+  if (s.dk == DK) {                                                     \
+    if (s.bf16)                                                         \
+      return s.dv == 64 ? launch_scan<__bf16, DK, CHB, 2>(s, a, st)     \
+                        : launch_scan<__bf16, DK, CHB, 1>(s, a, st);    \
+    return s.dv == 64 ? launch_scan<float, DK, 32, 2>(s, a, st)         \
+                      : launch_scan<float, DK, 32, 1>(s, a, st);        \
+  }
   GDN_SCAN_CASE(64, 64)
   GDN_SCAN_CASE(128, 64)
   GDN_SCAN_CASE(256, 32)

@@ -402,7 +402,8 @@ gdn_status_t gdn_conv_bwd(const void* x, const float* weight, const float* bias,
  *   C, B [N, H, dk], x, out [N, HV, dv] in qkv_dtype; dt [N, HV] fp32; A_log, dt_bias [HV] fp32;
  *   D [HV] fp32 or NULL for zero; state_pool [pool, HV, dv, dk] fp32, updated in place.
  * Evaluated in chunks on the matrix cores with fp32 sums: every factor keeps 24 bits in the
- * states, and in the outputs of fp32 inputs; one bf16 rounding in the outputs of bf16 inputs.
+ * states, and in the outputs of fp32 inputs; 16 bits in the outputs of bf16 inputs, which are
+ * then rounded to bf16, once.
  * Long requests are worked on in pieces, whose length goes by N, B and the shape alone. A
  * non-finite x also reaches that column of the up to 31 tokens before it in its request, and
  * need not reach the states behind its piece once its decay there is zero in fp32.
