@@ -46,7 +46,12 @@ __device__ __forceinline__ void load_weights(const float* __restrict__ weight,
                                              const float* __restrict__ bias, int c,
                                              float (&w)[W][VEC], float (&b)[VEC]) {
   float t[VEC * W];  // rows c .. c + VEC - 1 of [CH, W] are contiguous
-  load_vec<VEC * W>(weight + (int64_t)c * W, t);
+  if constexpr (VEC > 1) {
+    load_vec<VEC * W>(weight + (int64_t)c * W, t);
+  } else {  // only aligned to one weight
+#pragma unroll
+    for (int j = 0; j < W; ++j) t[j] = weight[(int64_t)c * W + j];
+  }
 #pragma unroll
   for (int j = 0; j < W; ++j)
 #pragma unroll
