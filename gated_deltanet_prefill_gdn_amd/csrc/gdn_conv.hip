@@ -617,7 +617,8 @@ hipError_t launch_conv_decode(const ConvShape& s, const void* x, const float* we
 }
 
 size_t conv_bwd_workspace(const ConvShape& s) {
-  // the scalar path's row count is the larger one of the two at a given shape
+  // whichever path serves the call: vectors have fewer column blocks, hence shorter runs and, up to
+  // four times, more partial rows
   ConvShape t = s;
   size_t rows = 0;
   for (const bool vec : {false, true}) {
