@@ -929,9 +929,13 @@ int short_tokens(const SsmShape& s) {
   return s.N <= 4 * s.B && s.B * s.HV * (s.dv / 64) >= 2048 ? 4 : 0;
 }
 
-// Segments of cut requests: each such request has more than lseg tokens, so at most twice
-// N / lseg segments in all.
-int64_t max_cut(const SsmShape& s, int lseg) { return lseg ? 2 * (s.N / lseg) : 0; }
+// Segments of cut requests: one of L tokens has at most L / lseg + 1, and each has more than lseg
+// tokens, so that there are at most min(B, N / lseg) of them.
+int64_t max_cut(const SsmShape& s, int lseg) {
+  if (!lseg) return 0;
+  const int64_t full = s.N / lseg;
+  return full + (s.B < full ? s.B : full);
+}
 
 struct ScanLayout {
   size_t state = 0, decay = 0, total = 0;
