@@ -171,18 +171,20 @@ __device__ __forceinline__ float softplusf(float x) {
   return fmaxf(x, 0.f) + (w == 1.f ? z : l);
 }
 
-// a and b as sums of P bf16 each (2^-8, 2^-17 or 2^-25 of them off), the parts of the two side by
-// side in a register: one conversion instruction takes both.
+// a and b as sums of P bf16 each, the parts of the two side by side in a register. All parts but the
+// last are cut off, not rounded, so that no finite value becomes infinite: two are 2^-16 of a value
+// off, three hold its 24 bits. (An infinite value leaves NaN in the last part.)
 template <int P>
 __device__ __forceinline__ void split(float a, float b, uint32_t (&part)[P]) {
+  static_assert(P > 1, "one part rounds, and may overflow");
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    part[p] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
-    if (p + 1 < P) {
-      a -= __uint_as_float(part[p] << 16);
-      b -= __uint_as_float(part[p] & 0xFFFF0000u);
-    }
+  for (int p = 0; p + 1 < P; ++p) {
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+    part[p] = __builtin_amdgcn_perm(ub, ua, 0x07060302);  // the upper halves of both
+    a -= __uint_as_float(ua & 0xFFFF0000u);
+    b -= __uint_as_float(ub & 0xFFFF0000u);
   }
+  part[P - 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
 // v from another lane of the same row of 16, chosen by a DPP control code; 0 from outside it.

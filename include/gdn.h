@@ -406,7 +406,8 @@ gdn_status_t gdn_conv_bwd(const void* x, const float* weight, const float* bias,
  * then rounded to bf16, once.
  * Long requests are worked on in pieces, whose length goes by N, B and the shape alone. A
  * non-finite x also reaches that column of the up to 31 tokens before it in its request, and
- * need not reach the states behind its piece once its decay there is zero in fp32.
+ * need not reach the states behind its piece once its decay there is zero in fp32. Every
+ * finite value is taken as it is; an infinite one may stand as NaN in whatever it reaches.
  * C, B, x, out and state_pool 16-byte aligned. workspace: at least gdn_ssm_workspace_size bytes,
  * 256-byte aligned; its contents on entry do not matter. N == 0 or B == 0 is a no-op. */
 size_t gdn_ssm_workspace_size(const gdn_problem_t* prob);
