@@ -171,18 +171,26 @@ __device__ __forceinline__ float softplusf(float x) {
   return fmaxf(x, 0.f) + (w == 1.f ? z : l);
 }
 
-// a and b as sums of P bf16 each, the parts of the two side by side in a register. All parts but the
-// last are cut off, not rounded, so that no finite value becomes infinite: two are 2^-16 of a value
-// off, three hold its 24 bits. (An infinite value leaves NaN in the last part.)
-template <int P>
+// a and b as sums of P bf16 each, the parts of the two side by side in a register. No finite value
+// becomes infinite. Parts are rounded where the other factor is a sum as well (PAIRS), so that what
+// its products leave out, the second part times the third, is below 2^-24 and of either sign; where
+// the other factor is exact they are cut off, which takes fewer instructions: two parts are then
+// 2^-16 of a value off, three hold its 24 bits. (An infinite value leaves NaN in a later part.)
+template <int P, bool PAIRS>
 __device__ __forceinline__ void split(float a, float b, uint32_t (&part)[P]) {
   static_assert(P > 1, "one part rounds, and may overflow");
+  constexpr float kTop = 0x1.FEp127f;  // the largest bf16
 #pragma unroll
   for (int p = 0; p + 1 < P; ++p) {
-    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    part[p] = __builtin_amdgcn_perm(ub, ua, 0x07060302);  // the upper halves of both
-    a -= __uint_as_float(ua & 0xFFFF0000u);
-    b -= __uint_as_float(ub & 0xFFFF0000u);
+    if constexpr (PAIRS) {
+      const f32x2 v = p ? f32x2{a, b} : f32x2{__builtin_amdgcn_fmed3f(a, -kTop, kTop),
+                                              __builtin_amdgcn_fmed3f(b, -kTop, kTop)};
+      part[p] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+    } else {
+      part[p] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
+    }
+    a -= __uint_as_float(part[p] << 16);
+    b -= __uint_as_float(part[p] & 0xFFFF0000u);
   }
   part[P - 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
@@ -305,8 +313,8 @@ struct Stage {
       } else {
         const f32x4 v = __builtin_bit_cast(f32x4, r[i]);
         uint32_t lo[NP], hi[NP];
-        split<NP>(v[0], v[1], lo);
-        split<NP>(v[2], v[3], hi);
+        split<NP, true>(v[0], v[1], lo);
+        split<NP, true>(v[2], v[3], hi);
 #pragma unroll
         for (int p = 0; p < NP; ++p)
           *reinterpret_cast<u32x2*>(to + p * plane + row * ld + c) = u32x2{lo[p], hi[p]};
@@ -603,8 +611,8 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
                   *reinterpret_cast<u32x2*>(to + p * kTileP + 4) = u32x2{0, 0};
             }
             uint32_t lo[PS], hi[PS];
-            split<PS>(v[0], v[1], lo);
-            split<PS>(v[2], v[3], hi);
+            split<PS, F32>(v[0], v[1], lo);
+            split<PS, F32>(v[2], v[3], hi);
 #pragma unroll
             for (int p = 0; p < PS; ++p)
               *reinterpret_cast<u32x2*>(to + p * kTileP) = u32x2{lo[p], hi[p]};
@@ -635,7 +643,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
           for (int e = 0; e < 8; e += 2) {
             uint32_t part[PS];
             const acc4 v = st[2 * k + e / 4][pt];
-            split<PS>(v[e % 4], v[e % 4 + 1], part);
+            split<PS, F32>(v[e % 4], v[e % 4 + 1], part);
 #pragma unroll
             for (int p = 0; p < PS; ++p) words[p][e / 2] = part[p];
           }
@@ -681,6 +689,9 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
       const __bf16* const ph = s_p + hw * PS * kTileP;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
+        acc4 yp[2];  // fp32 keeps the two sums apart: fewer roundings at the size of the output
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt) yp[pt] = F32 ? acc4{0.f, 0.f, 0.f, 0.f} : y[t][pt];
 #pragma unroll
         for (int k = 0; k <= t / 2; ++k)
 #pragma unroll
@@ -690,7 +701,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 #pragma unroll
             for (int p = 0; p < NP && p + q < PS; ++p)
 #pragma unroll
-              for (int pt = 0; pt < 2; ++pt) y[t][pt] = mma_bf16(xf[p][pt][k], pf, y[t][pt]);
+              for (int pt = 0; pt < 2; ++pt) yp[pt] = mma_bf16(xf[p][pt][k], pf, yp[pt]);
           }
         // + D x, and out: four columns of one token per lane
         const int row = 16 * t + r;
@@ -706,7 +717,10 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
               xv[i] = p == NP - 1 ? (float)xp[i] : xv[i] + (float)xp[i];
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(dskip, xv[i], y[t][pt][i]);
+          for (int i = 0; i < 4; ++i) {
+            o[i] = __builtin_fmaf(dskip, xv[i], yp[pt][i]);
+            if constexpr (F32) o[i] += y[t][pt][i];
+          }
           const int to = row * (int)(ldx * sizeof(T)) + (16 * pt + 4 * g) * (int)sizeof(T);
           if constexpr (F32) {
             __builtin_amdgcn_raw_buffer_store_b128(
@@ -747,7 +761,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
             for (int p = NP - 2; p >= 0; --p) v[i] += (float)xf[p][pt][k][e + i];
           }
           uint32_t part[NU];
-          split<NU>(v[0] * w[0], v[1] * w[1], part);
+          split<NU, F32>(v[0] * w[0], v[1] * w[1], part);
 #pragma unroll
           for (int p = 0; p < NU; ++p) xw[p][pt][e / 2] = part[p];
         }
