@@ -46,3 +46,16 @@ def test_four_parts_of_a_piece_at_large_state_sizes(dtype, dk, dv, hv):
     check(c, dtype, out[:, heads], pool[:, heads], what)
     if dtype == "bf16":
         check_rounding(c, out[:, heads], what)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths", [[1, 0, 700, 3] + [1] * 150, [1] * 150 + [300]], ids=["chunks", "tokens"])
+def test_one_prompt_beside_many_single_tokens(dtype, lengths):
+    """So many requests that none is cut: the single tokens in chunks, or, where the mean length says
+    so, token by token."""
+    c = make(23, lengths, 8, 64, 64, 64, dtype)
+    out, pool = call(c)
+    what = f"ssm {dtype} {max(lengths)} tokens beside single ones"
+    check(c, dtype, out, pool, what)
+    if dtype == "bf16":
+        check_rounding(c, out, what)
