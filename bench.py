@@ -94,7 +94,8 @@ def kernel_source_hash(kind: str = "prefill") -> str:
     """sha256[:16] over the kernel sources a measurement depends on: for "prefill" (the
     bf16 path) every .hip / .h file of csrc except the decode, Promote, backward, fp32 and
     layer kernels' own files, for "prefill_f32" PREFILL_F32_SOURCES, for "decode" DECODE_SOURCES,
-    for "promote" PROMOTE_SOURCES, for "backward" BACKWARD_SOURCES."""
+    for "promote" PROMOTE_SOURCES, for "backward" BACKWARD_SOURCES, for "layer" LAYER_SOURCES
+    and gdn_mfma.h."""
     csrc = os.path.join(ROOT, "gated_deltanet_prefill_gdn_amd", "csrc")
     if kind == "decode":
         files = sorted(DECODE_SOURCES)
@@ -104,6 +105,8 @@ def kernel_source_hash(kind: str = "prefill") -> str:
         files = sorted(BACKWARD_SOURCES)
     elif kind == "prefill_f32":
         files = sorted(PREFILL_F32_SOURCES)
+    elif kind == "layer":
+        files = sorted((*LAYER_SOURCES, "gdn_mfma.h"))
     else:
         files = sorted(f for f in os.listdir(csrc) if f.endswith((".hip", ".h"))
                        and f not in ("gdn_decode.hip", "gdn_promote.hip", "gdn_backward.hip",

@@ -14,8 +14,10 @@
 // forms the row's statistics again from x, which it has to read anyway, so the forward keeps
 // nothing for it. Measured: forward 33860 x 32 gated rows of 128, bf16, 155 us (5.4 TB/s);
 // gradients of 16384 x 16 such rows 61 us (5.5 TB/s) and 6 for the sums, of 16384 rows of 4096 87
-// us (4.9 TB/s) and 9. A short row takes 8 to 64 threads, so that all loads of a wave are one
-// vector a thread and the sums stay in a wave; longer ones a workgroup.
+// us (4.9 TB/s) and 9. Gradients of rows above 8192 entries, and of rows above 4096 element by
+// element, run out of registers and spill: 8192 rows of 16384, gated, 522 us (2.6 TB/s), of 4097
+// 226. A short row takes 8 to 64 threads, so that all loads of a wave are one vector a thread and
+// the sums stay in a wave; longer ones a workgroup.
 #include "gdn_layer.h"
 
 namespace gdn {
@@ -86,7 +88,7 @@ __device__ __forceinline__ void load_cols(const T* p, const int (&col)[NC], cons
 }
 
 // The same as they are stored, for rows that wait in registers: with the backward's rows loaded as
-// they are and converted at their use its gated rows of 128 take 64 us instead of 94.
+// they are and converted at their use 16384 x 16 gated rows of 128 take 71 us a call, not 81.
 template <typename T, int VEC, int NC>
 __device__ __forceinline__ void load_raw(const T* p, const int (&col)[NC], const bool (&in)[NC],
                                          Raw<T, VEC> (&v)[NC]) {
@@ -372,9 +374,10 @@ int rows_per_block(const Pick& p) { return p.tpr > 256 ? 1 : 256 / p.tpr; }
 
 // Workgroups of a launch; the rest of the rows in the kernel's loop, which keeps the weights (and
 // the gradients' sums) in registers. Forward: the more the better (33860 x 32 rows of 128, gated:
-// 159 us with 16384, 168 with 4096; the next row's loads ahead of this row's work took 169).
+// 154 us with 16384, 161 with 4096; the next row's loads ahead of this row's work took 6 % more).
 // Backward: each writes a partial row of dweight and dbias, and 768 are what the device holds
-// (16384 rows of 4096: 107 us with 768 and with 1024, 111 with 512; heads of 128: 69, 71 and 77).
+// (us a call with 512, 768 and 1024: 16384 rows of 4096 105, 93 and 103; 16384 x 16 heads of 128 76,
+// 71 and 73).
 int64_t fwd_blocks(const NormShape& s, const Pick& p) {
   const int64_t all = cdiv(s.N * s.heads, rows_per_block(p));
   return all < 16384 ? all : 16384;

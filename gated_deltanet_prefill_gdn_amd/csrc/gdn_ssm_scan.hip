@@ -815,10 +815,10 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 
 // The pieces' states (OUTPUT false); the outputs of pieces, and whole requests.
 // Workgroups of a CU that the registers are held to (fp32: LDS for one at dk >= 128): outputs
-// keep the next C, the scores and a bf16 state in them too, states alone leave room for three (8
-// ragged requests, 64 heads of 64 x 128: 112 us, with two 136). At dk = 256 a compiler left free
-// takes more than half the registers, and one workgroup a CU: 16384 tokens, 8 heads of 256 x 256,
-// 176 us instead of 158, 10 ragged requests 462 instead of 273.
+// keep the next C, the scores and the states' parts in them too, states alone leave room for three
+// (8 ragged requests, 64 heads of 64 x 128: 412 us a call, with two 425). At dk = 256 a compiler left
+// free takes more than half the registers, and one workgroup a CU: 16384 tokens, 8 heads of 256 x
+// 256, 230 us instead of 179, 10 ragged requests 451 instead of 324.
 template <typename T, int DK, bool OUTPUT>
 constexpr int kGroupsPerCU = sizeof(T) == 4 ? 1 : OUTPUT || DK == 256 ? 2 : 3;
 template <typename T, int DK, int CH, int HEADS, bool OUTPUT>
@@ -910,11 +910,14 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(ScanArgs a, int plane, in
 // half a piece more for every request, k = 1 .. 4: more rounds even out pieces of different
 // lengths, fewer spare the joins, which cost what kPieceTokens tokens do (a piece's state is
 // written, joined and read: 256 KB at dk = 128 for 128 columns, whose tokens take 0.75 KB; with
-// 350 instead of 1000, 8 ragged requests of 33860 tokens in all, 64 heads of 64 x 128, take 438
-// us instead of 408, and 16 requests of 1024 are cut for nothing, 140 us instead of 103).
+// 350 instead of 1000, 8 ragged requests of 33860 tokens in all, 64 heads of 64 x 128, take 432
+// us instead of 412, and 16 requests of 1024 are cut for nothing, 231 us instead of 155).
+// Requests that fill the device by their number alone (from 4096 / blocks of them on) are not cut:
+// equal ones need not be, but a long one among them is walked by one workgroup a column block. A
+// prompt of 32768 tokens beside 125 single tokens, heads as above, takes 2.85 ms, alone 0.37 ms.
 // A piece's state in one part, two or four, by its length: one request of 131072 tokens, 32 heads
-// of 128 x 128 (pieces of 8512), 367, 317 and 296 us for states and join; pieces of 2880 160, 155
-// and 163; pieces of 1216 174, 192 and 239.
+// of 128 x 128 (pieces of 8512), 1144, 1106 and 1081 us a call; the 8 ragged requests (of 2880) 428,
+// 411 and 421; 16384 tokens, 8 heads of 256 x 256 (of 576), 178, 198 and 227.
 constexpr int kPieceTokens = 1000;
 struct Cut {
   int lseg, parts;
@@ -939,8 +942,8 @@ Cut cut_of(const SsmShape& s) {
 
 // Requests of at most this many tokens run token by token, where the mean length says that most
 // are and there are enough to fill the device (a call that splits pays a launch for the longer
-// ones too): 512 requests of 4 tokens, 32 heads of 128 x 128, take 401 us there, of 8 tokens 559;
-// in chunks requests of 6 take 456 and of 8 454.
+// ones too): 512 requests of 4 tokens, 32 heads of 128 x 128, take 392 us there and 438 in chunks,
+// of 8 tokens 570 and 445.
 int short_tokens(const SsmShape& s) {
   return s.N <= 4 * s.B && s.B * s.HV * (s.dv / 64) >= 2048 ? 4 : 0;
 }

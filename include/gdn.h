@@ -404,10 +404,13 @@ gdn_status_t gdn_conv_bwd(const void* x, const float* weight, const float* bias,
  * Evaluated in chunks on the matrix cores with fp32 sums: every factor keeps 24 bits in the
  * states, and in the outputs of fp32 inputs; 16 bits in the outputs of bf16 inputs, which are
  * then rounded to bf16, once.
- * Long requests are worked on in pieces, whose length goes by N, B and the shape alone. A
- * non-finite x also reaches that column of the up to 31 tokens before it in its request, and
- * need not reach the states behind its piece once its decay there is zero in fp32. Every
- * finite value is taken as it is; an infinite one may stand as NaN in whatever it reaches.
+ * Long requests are worked on in pieces, whose length goes by N, B and the shape alone. In a batch
+ * of many requests (from about 4096 / (H ceil(HV dv / (128 H))) on) none is cut: a long one among
+ * them is walked from end to end, and is better called by itself.
+ * A non-finite x also reaches that column of the up to 31 tokens before it in its request, and need
+ * not reach the states behind its piece once its decay there is zero in fp32. Every finite value is
+ * taken as it is; an infinite one may stand as NaN in whatever it reaches.
+ * There is no backward call.
  * C, B, x, out and state_pool 16-byte aligned. workspace: at least gdn_ssm_workspace_size bytes,
  * 256-byte aligned; its contents on entry do not matter. N == 0 or B == 0 is a no-op. */
 size_t gdn_ssm_workspace_size(const gdn_problem_t* prob);
