@@ -103,7 +103,8 @@ __global__ __launch_bounds__(kTokenThreads) void ssm_token_kernel(
     s[j][1] =
         __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(sp + j * RPW * DK + DK / 2));
   }
-  const float decay = expf(A_log[hv]), dtb = dt_bias[hv], dd = D ? D[hv] : 0.f;
+  const float rate = expf(A_log[hv]), dtb = dt_bias[hv], dd = D ? D[hv] : 0.f;
+  const float decay = rate > 3e38f ? 3e38f : rate;  // finite, so that no step means no decay
   for (; t < t_end; ++t) {
     const int64_t th = t * HV + hv;
     float bb[8], cc[8], xr[NR];

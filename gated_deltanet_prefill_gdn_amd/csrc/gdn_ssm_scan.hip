@@ -165,6 +165,9 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // are kept to base 2.
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// x, or lo where it is below that. (NaN stays NaN.)
+__device__ __forceinline__ float above(float x, float lo) { return x < lo ? lo : x; }
+
 // log(1 + e^x) = max(x, 0) + log1p(z), z = e^-|x|: with w = 1 + z rounded, log1p(z) is
 // log(w) z / (w - 1), in which the rounding of w cancels, and z where w is 1.
 __device__ __forceinline__ float softplusf(float x) {
@@ -435,7 +438,7 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
       st[s][pt] = OUT && live ? *reinterpret_cast<const acc4*>(from + 16 * pt * DK + 16 * s)
                               : acc4{0.f, 0.f, 0.f, 0.f};
 
-  const float decay = -expf(a.A_log[hv0 + gh]) * kLog2e, dtb = a.dt_bias[hv0 + gh];
+  const float decay = above(-expf(a.A_log[hv0 + gh]) * kLog2e, -3e38f), dtb = a.dt_bias[hv0 + gh];
   const float dskip = a.D ? a.D[hv] : 0.f;
   // a piece's state: sum of g from the chunks walked to the piece's end, of each head
   float behind[HEADS] = {};
@@ -447,7 +450,8 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 #pragma unroll
       for (int hh = 0; hh < HEADS; ++hh) {
         if (hh >= nh) break;
-        const float rate = -expf(a.A_log[hv0 + hh]) * kLog2e, shift = a.dt_bias[hv0 + hh];
+        const float rate = above(-expf(a.A_log[hv0 + hh]) * kLog2e, -3e38f);
+        const float shift = a.dt_bias[hv0 + hh];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int64_t k = t + u * kThreads + tid;
@@ -521,7 +525,8 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
       G& gt = gate_set(gh, chunk + gc);
       const bool in = lane < CH && chunk + gc < chunks && place(chunk + gc) + lane < sg.t1;
       const float step = in ? softplusf(qdt + dtb) : 0.f;
-      const float gl = in ? decay * step : 0.f;
+      // (a g of -1e30 decays to zero as any lower one does, and sums of them stay finite)
+      const float gl = in ? above(decay * step, -1e30f) : 0.f;
       const R local = row_prefix((R)gl);
       R at[NT + 1];  // G before each tile, and at the end
       at[0] = 0;
