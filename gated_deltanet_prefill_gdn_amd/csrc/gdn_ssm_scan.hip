@@ -29,7 +29,7 @@
 // (errors of 1.79e-3 of the outputs' size instead of 1.66e-3, twelve times a rounding where terms
 // cancel; the two cases below took 1009 and 364 us a call with it). For fp32 inputs every operand is three bf16 and
 // a product takes the six pairs of parts that reach 2^-24: 2.7 times the rate of the fp32 matrix
-// instructions. Gates and their sums are fp32 (fp32 inputs: G of a chunk's outputs in fp64), and
+// instructions. Gates are fp32, the sums that differences are taken of fixed point or fp64, and
 // exponents are only taken of differences that are not positive, so strong decays underflow to zero
 // and nothing overflows.
 //
@@ -244,9 +244,13 @@ __device__ __forceinline__ double lane_of(double v, int lane) {
 }
 
 // The gates of one head in one chunk, an entry per token.
+// Outputs take e to differences of running sums of g (to base 2, as every g here), which go into the
+// thousands where some tokens erase a state that those between them keep: fp32 sums would leave
+// errors of up to 2^-10 there. fp32 inputs: the sum from the chunk's start in fp64. bf16 inputs: from
+// the tile's start in steps of 2^-19 (2^-16 off over a tile at most), whose differences are exact.
 template <int CH, typename R>
 struct Gates {
-  R G[CH];             // running sum of g in the chunk (to base 2, as every sum of g here)
+  R G[CH];
   float step[CH];      // d
   float eG[CH];        // e^G
   float row[CH];       // e^{G_t - G at the start of t's tile}
@@ -359,7 +363,7 @@ struct Dims {
   // no conflicts and 4.9 cycles where it is 8 mod 16 words, 8 elsewhere (measured).
   static constexpr int LDC = DK + 12, LDB = DK + 16, LDX = kColsBlock + 16, LDP = CH + 8;
   static constexpr int TileC = CH * LDC, TileB = CH * LDB, TileX = CH * LDX, TileP = CH * LDP;
-  using R = typename std::conditional<sizeof(T) == 4, double, float>::type;
+  using R = typename std::conditional<sizeof(T) == 4, double, int>::type;
   using G = Gates<CH, R>;
   // LDS: B, x, four gate sets; with outputs also C and the heads' decayed scores. For bf16 inputs
   // those of two heads start in C's place, which has been read by then: two workgroups a CU have
@@ -508,9 +512,10 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
 
   for (int chunk = 0; chunk < chunks; ++chunk) {
     const int64_t t0 = place(chunk);
-    if constexpr (MODE == kWhole) {
+    if constexpr (MODE == kWhole || (MODE == kOutput && HEADS == 2)) {
       // Places in LDS are formed anew for every chunk: kept in registers they spill, and a
-      // reload waits for the next chunk's rows, which were asked for before it.
+      // reload waits for the next chunk's rows, which were asked for before it (8 ragged requests
+      // with two heads a workgroup 477 us, so 418).
       asm volatile("" : "+v"(lane));
       r = lane & 15;
       g = lane >> 4;
@@ -527,30 +532,38 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
       const float step = in ? softplusf(qdt + dtb) : 0.f;
       // (a g of -1e30 decays to zero as any lower one does, and sums of them stay finite)
       const float gl = in ? above(decay * step, -1e30f) : 0.f;
-      const R local = row_prefix((R)gl);
-      R at[NT + 1];  // G before each tile, and at the end
+      using S = typename std::conditional<F32, double, float>::type;
+      const S local = row_prefix((S)gl);
+      S at[NT + 1];  // G before each tile, and at the end
       at[0] = 0;
 #pragma unroll
       for (int k = 0; k < NT; ++k) at[k + 1] = at[k] + lane_of(local, 16 * k + 15);
-      float after = 0.f;  // of g in the tiles behind this lane's
-      R mine = at[0];
-#pragma unroll
-      for (int k = NT - 1; k > 0; --k)
-        after += lane < 16 * k ? lane_of((float)local, 16 * k + 15) : 0.f;
+      S mine = at[0];
 #pragma unroll
       for (int k = 1; k < NT; ++k) mine = lane >= 16 * k ? at[k] : mine;
+      const S Gp = mine + local;
+      const float behind_me = row_behind(gl);  // of g in this lane's tile
+      float tiles = 0.f;  // of g in the tiles behind this lane's, up to tile k
+#pragma unroll
+      for (int k = 1; k < NT; ++k) {
+        if constexpr (OUT)
+          if (lane < 16 * k)
+            gt.col[G::at(k) + lane] =
+                step * exp2_(F32 ? (float)(at[k] - Gp) : behind_me + tiles);
+        tiles += lane < 16 * k ? (float)lane_of(local, 16 * k + 15) : 0.f;
+      }
       if (lane < CH) {
         if constexpr (OUT) {
-          const R Gp = mine + local;
-          gt.G[lane] = Gp;
+          // (what is below 2^-160 is zero, and sixteen of it fit)
+          if constexpr (F32)
+            gt.G[lane] = Gp;
+          else
+            gt.G[lane] = row_prefix((int)__builtin_rintf(fmaxf(gl, -160.f) * 0x1p19f));
           gt.step[lane] = step;
           gt.eG[lane] = exp2_((float)Gp);
           gt.row[lane] = exp2_((float)local);
-#pragma unroll
-          for (int k = 1; k < NT; ++k)
-            if (lane < 16 * k) gt.col[G::at(k) + lane] = step * exp2_((float)(at[k] - Gp));
         }
-        gt.w[lane] = step * exp2_(row_behind(gl) + after);
+        gt.w[lane] = step * exp2_(behind_me + tiles);
       }
       if (lane == 0) gt.total[0] = (float)at[NT];
       fetch_dt(chunk + batch);
@@ -608,7 +621,8 @@ __device__ __forceinline__ void scan_segment(const ScanArgs& a, const Segment& s
               for (int e = 0; e < 4; ++e) Gj[e] = gs.G[16 * jt + 4 * g + e];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                float ex = sc[i][e] * (exp2_((float)(Gt - Gj[e])) * d[e]);
+                const float lag = (float)(Gt - Gj[e]) * (F32 ? 1.f : 0x1p-19f);
+                float ex = sc[i][e] * (exp2_(lag) * d[e]);
                 asm volatile("" : "+v"(ex));  // no branch around each entry
                 v[e] = 4 * g + e <= r ? ex : 0.f;
               }
