@@ -27,16 +27,16 @@
 // two bf16 (16 bits): the decayed scores, the state that S C reads, and the decayed x where a piece's
 // state is only formed to be read so. One bf16 each would be a rounding as large as the output's own
 // (errors of 1.79e-3 of the outputs' size instead of 1.66e-3, twelve times a rounding where terms
-// cancel; the two cases below took 1009 and 364 us a call with it). For fp32 inputs every operand is three bf16 and
+// cancel; the two cases below took 982 and 362 us a call with it). For fp32 inputs every operand is three bf16 and
 // a product takes the six pairs of parts that reach 2^-24: 2.7 times the rate of the fp32 matrix
 // instructions. Gates are fp32, the sums that differences are taken of fixed point or fp64, and
 // exponents are only taken of differences that are not positive, so strong decays underflow to zero
 // and nothing overflows.
 //
-// Measured, bf16, calls back to back: 131072 tokens, 32 heads of 128 x 128, 1197 us (outputs 947, 3.8
+// Measured, bf16, calls back to back: 131072 tokens, 32 heads of 128 x 128, 1164 us (outputs 919, 3.9
 // TB/s of what they move); 8 ragged requests of 33860 tokens, 64 heads of 64 x 128 that share C and B
-// by eights, 417 us (outputs 301). No unit is full in the outputs: the matrix cores are busy 36 and
-// 25 % of the time, the vector units 46 and 37, LDS 42 and 32. Two waves a SIMD and two or three
+// by eights, 425 us (outputs 307). No unit is full in the outputs: the matrix cores are busy 36 and
+// 24 % of the time, the vector units 46 and 38, LDS 42 and 31. Two waves a SIMD and two or three
 // barriers a chunk leave waits open, and behind the longest piece of the ragged requests a fifth of
 // the device idles.
 #include <type_traits>
