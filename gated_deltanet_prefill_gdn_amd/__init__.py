@@ -58,6 +58,9 @@ EXPORTED = ("gdn_prefill_workspace_size", "gdn_prefill_state_schedule", "gdn_pre
             "gdn_conv_fwd", "gdn_conv_decode_fwd", "gdn_conv_bwd_workspace_size", "gdn_conv_bwd",
             "gdn_ssm_workspace_size", "gdn_ssm_prefill_fwd", "gdn_ssm_decode_fwd",
             "gdn_norm_fwd", "gdn_norm_bwd_workspace_size", "gdn_norm_bwd",
+            "gdn_linear_workspace_size", "gdn_linear_prefill_fwd", "gdn_linear_decode_fwd",
+            "gdn_linear_bwd_workspace_size", "gdn_linear_bwd",
+            "gdn_adapter_workspace_size", "gdn_adapter_fwd", "gdn_adapter_decode_fwd",
             "gdn_status_str", "gdn_version")
 
 
@@ -83,6 +86,41 @@ class GdnPromoteProblem(ctypes.Structure):
         ("head_k", ctypes.c_int32),
         ("head_v", ctypes.c_int32),
         ("kv_dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class GdnLinearProblem(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", ctypes.c_int64),
+        ("batch", ctypes.c_int64),
+        ("pool_size", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("num_qk_heads", ctypes.c_int32),
+        ("num_v_heads", ctypes.c_int32),
+        ("head_k", ctypes.c_int32),
+        ("head_v", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class GdnAdapterProblem(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", ctypes.c_int64),
+        ("batch", ctypes.c_int64),
+        ("x_stride", ctypes.c_int64),
+        ("base_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+        ("inputs", ctypes.c_int32),
+        ("outputs", ctypes.c_int32),
+        ("rank", ctypes.c_int32),
+        ("adapters", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
     ]
 
@@ -138,8 +176,9 @@ def load_library(path: str = LIB_PATH):
     L.gdn_status_str.argtypes = [ctypes.c_int]
     L.gdn_version.restype = ctypes.c_int32
     L.gdn_version.argtypes = []
-    from . import layer
-    layer.declare(L)
+    from . import adapter, layer, linear
+    for module in (layer, linear, adapter):
+        module.declare(L)
     if path == LIB_PATH:
         _lib = L
     return L
@@ -493,17 +532,23 @@ def gdn_validate_inputs(cu_seqlens, cache_indices, prob: GdnProblem, stream=None
                                                   ctypes.byref(prob), ctypes.c_void_p(st)))
 
 
-# The layer operators (layer.py imports torch, which this module only does when it is called).
+# The layer operators (their modules import torch, which this module only does when it is called).
 _LAYER = ("GDN_CONV_SILU", "GDN_NORM_RMS", "GDN_NORM_GATE_FIRST", "GdnConvProblem",
           "GdnNormProblem", "conv_problem", "norm_problem", "gdn_conv_fwd",
           "gdn_conv_decode_fwd", "gdn_conv_bwd_workspace_size", "gdn_conv_bwd",
           "gdn_ssm_workspace_size", "gdn_ssm_prefill_fwd", "gdn_ssm_decode_fwd", "gdn_norm_fwd",
           "gdn_norm_bwd_workspace_size", "gdn_norm_bwd")
+_LINEAR = ("linear_problem", "gdn_linear_workspace_size", "gdn_linear_prefill_fwd",
+           "gdn_linear_decode_fwd", "gdn_linear_bwd_workspace_size", "gdn_linear_bwd")
+_ADAPTER = ("adapter_problem", "gdn_adapter_workspace_size", "gdn_adapter_fwd",
+            "gdn_adapter_decode_fwd")
 
 
 def __getattr__(name):
-    if name in _LAYER:
-        from . import layer
-        globals().update({n: getattr(layer, n) for n in _LAYER})
-        return globals()[name]
+    import importlib
+    for module, names in (("layer", _LAYER), ("linear", _LINEAR), ("adapter", _ADAPTER)):
+        if name in names:
+            found = importlib.import_module("." + module, __name__)
+            globals().update({n: getattr(found, n) for n in names})
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

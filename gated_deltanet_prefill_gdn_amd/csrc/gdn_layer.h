@@ -1,5 +1,6 @@
 // Internal declarations of the layer operators around the recurrence: short causal
-// convolution, selective state space scan, gated norm. Not part of the public C ABI.
+// convolution, selective state space scan, gated norm, linear attention, low-rank adapters. Not part of the
+// public C ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -184,6 +185,43 @@ hipError_t launch_ssm_short(const SsmShape& s, const void* C, const void* B, con
                             const float* dt, const float* A_log, const float* dt_bias,
                             const float* D, float* state, const int64_t* idx, const int64_t* cu,
                             void* out, int64_t max_len, hipStream_t st);
+
+// ---- linear attention
+struct LinearShape {
+  int64_t N, B, pool;
+  int64_t ldq, ldk, ldv;  // elements between tokens
+  int H, HV, dk, dv;
+  bool bf16;
+  float scale;
+};
+size_t linear_workspace(const LinearShape& s);
+size_t linear_bwd_workspace(const LinearShape& s);
+bool linear_prefill_grids_fit(const LinearShape& s);
+bool linear_decode_grid_fits(const LinearShape& s);
+bool linear_bwd_grids_fit(const LinearShape& s);
+hipError_t launch_linear_prefill(const LinearShape& s, const void* q, const void* k, const void* v,
+                                 const float* log_decay, float* state, const int64_t* idx,
+                                 const int64_t* cu, void* out, char* ws, hipStream_t st);
+hipError_t launch_linear_decode(const LinearShape& s, const void* q, const void* k, const void* v,
+                                const float* log_decay, float* state, const int64_t* idx,
+                                void* out, hipStream_t st);
+hipError_t launch_linear_bwd(const LinearShape& s, const void* q, const void* k, const void* v,
+                             const float* log_decay, const float* state, const int64_t* idx,
+                             const int64_t* cu, const void* dout, const float* dstate, void* dq,
+                             void* dk, void* dv, float* dstate0, char* ws, hipStream_t st);
+
+// ---- low-rank adapters
+struct AdapterShape {
+  int64_t N, B, ldx, ldbase, ldout;
+  int K, M, R, adapters;
+  bool bf16;
+};
+size_t adapter_workspace(const AdapterShape& s);
+bool adapter_grids_fit(const AdapterShape& s);
+// cu NULL: row b belongs to request b
+hipError_t launch_adapter(const AdapterShape& s, const void* x, const void* base, const void* A,
+                          const void* B, const float* scaling, const int64_t* idx,
+                          const int64_t* cu, void* out, char* ws, hipStream_t st);
 
 }  // namespace layer
 }  // namespace gdn

@@ -1,5 +1,8 @@
 // C ABI of the layer operators (declared in include/gdn.h): host-side argument checks and
-// launches of the short causal convolution, the selective state space scan and the gated norm.
+// launches of the short causal convolution, the selective state space scan, the gated norm,
+// linear attention and the low-rank adapters.
+#include <math.h>
+
 #include "gdn.h"
 #include "gdn_layer.h"
 
@@ -116,6 +119,71 @@ gdn_status_t check_norm(const gdn_norm_problem_t* p, bool gated, bool backward, 
   s->vec = s->dim % v == 0 && s->x_stride % v == 0 && (!gated || s->z_stride % v == 0) &&
            (!gated || !backward || s->dz_stride % v == 0);
   return GDN_OK;
+}
+
+gdn_status_t check_linear(const gdn_linear_problem_t* p, LinearShape* s) {
+  if (!p || p->flags != 0 || p->reserved != 0) return GDN_ERR_INVALID_ARG;
+  if (p->total_tokens < 0 || p->batch < 0 || p->pool_size < 0) return GDN_ERR_INVALID_ARG;
+  if (p->num_qk_heads <= 0 || p->num_v_heads <= 0 || p->num_v_heads % p->num_qk_heads != 0)
+    return GDN_ERR_INVALID_ARG;
+  if (p->head_k <= 0 || p->head_v <= 0 || !dtype_ok(p->dtype) || !isfinite(p->scale))
+    return GDN_ERR_INVALID_ARG;
+  for (const int32_t d : {p->head_k, p->head_v})
+    if (d != 64 && d != 128 && d != 256) return GDN_ERR_UNSUPPORTED;
+  if (p->num_v_heads > 65535 || p->batch > ((int64_t)1 << 30) ||
+      p->pool_size > ((int64_t)1 << 31) || p->total_tokens > ((int64_t)1 << 30))
+    return GDN_ERR_UNSUPPORTED;
+  *s = LinearShape{p->total_tokens, p->batch,        p->pool_size,   p->q_stride, p->k_stride,
+                   p->v_stride,     p->num_qk_heads, p->num_v_heads, p->head_k,   p->head_v,
+                   p->dtype == GDN_DTYPE_BF16,       p->scale};
+  const int v = vec(s->bf16);
+  const int64_t qk = (int64_t)s->H * s->dk, vv = (int64_t)s->HV * s->dv;
+  if (s->ldq < qk || s->ldk < qk || s->ldv < vv) return GDN_ERR_INVALID_ARG;
+  for (const int64_t ld : {s->ldq, s->ldk, s->ldv}) {
+    if (ld % v != 0) return GDN_ERR_INVALID_ARG;
+    if (ld > ((int64_t)1 << 22)) return GDN_ERR_UNSUPPORTED;  // 64 rows stay below 2^31 bytes
+  }
+  if (qk > ((int64_t)1 << 22) || vv > ((int64_t)1 << 22)) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+gdn_status_t check_adapter(const gdn_adapter_problem_t* p, AdapterShape* s) {
+  if (!p || p->reserved != 0) return GDN_ERR_INVALID_ARG;
+  if (p->total_tokens < 0 || p->batch < 0 || !dtype_ok(p->dtype)) return GDN_ERR_INVALID_ARG;
+  if (p->inputs <= 0 || p->outputs <= 0 || p->rank <= 0 || p->adapters < 0)
+    return GDN_ERR_INVALID_ARG;
+  if (p->x_stride < p->inputs || p->base_stride < p->outputs || p->out_stride < p->outputs)
+    return GDN_ERR_INVALID_ARG;
+  if (p->rank > 128 || p->adapters > 4096 || p->inputs > (1 << 20) || p->outputs > (1 << 20) ||
+      p->total_tokens > ((int64_t)1 << 30) || p->batch > ((int64_t)1 << 30) ||
+      p->x_stride > ((int64_t)1 << 30) || p->base_stride > ((int64_t)1 << 30) ||
+      p->out_stride > ((int64_t)1 << 30))
+    return GDN_ERR_UNSUPPORTED;
+  *s = AdapterShape{p->total_tokens, p->batch,   p->x_stride, p->base_stride, p->out_stride,
+                    p->inputs,       p->outputs, p->rank,     p->adapters,
+                    p->dtype == GDN_DTYPE_BF16};
+  return GDN_OK;
+}
+
+gdn_status_t run_adapter(const void* x, const void* base, const void* A, const void* B,
+                         const float* scaling, const int64_t* idx, const int64_t* cu, void* out,
+                         const gdn_adapter_problem_t* prob, bool decode, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  AdapterShape s;
+  const gdn_status_t ps = check_adapter(prob, &s);
+  if (ps != GDN_OK) return ps;
+  if (decode && s.N != s.B) return GDN_ERR_INVALID_ARG;
+  if (s.N == 0 || s.B == 0) return GDN_OK;
+  if (!x || !base || !out || !idx || (!decode && !cu)) return GDN_ERR_INVALID_ARG;
+  if (s.adapters > 0 && (!A || !B || !scaling)) return GDN_ERR_INVALID_ARG;
+  if (base == out && s.ldbase != s.ldout) return GDN_ERR_INVALID_ARG;
+  if (!adapter_grids_fit(s)) return GDN_ERR_UNSUPPORTED;
+  const size_t need = adapter_workspace(s);
+  if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255) != 0))
+    return GDN_ERR_WORKSPACE;
+  const hipError_t e = launch_adapter(s, x, base, A, B, scaling, idx, decode ? nullptr : cu, out,
+                                      (char*)workspace, (hipStream_t)stream);
+  return e == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 
 }  // namespace
@@ -262,6 +330,106 @@ gdn_status_t gdn_norm_bwd(const void* x, const float* weight, const float* bias,
   const hipError_t e = launch_norm_bwd(s, x, weight, bias, z, dout, dx, dz, dweight, dbias,
                                        (float*)workspace, (hipStream_t)stream);
   return e == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+size_t gdn_linear_workspace_size(const gdn_linear_problem_t* prob) {
+  LinearShape s;
+  return check_linear(prob, &s) == GDN_OK ? linear_workspace(s) : 0;
+}
+
+gdn_status_t gdn_linear_prefill_fwd(const void* q, const void* k, const void* v,
+                                    const float* log_decay, float* state_pool,
+                                    const int64_t* cache_indices, const int64_t* cu_seqlens,
+                                    void* out, const gdn_linear_problem_t* prob, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  LinearShape s;
+  const gdn_status_t ps = check_linear(prob, &s);
+  if (ps != GDN_OK) return ps;
+  if (s.N == 0 || s.B == 0) return GDN_OK;
+  if (!q || !k || !v || !log_decay || !cu_seqlens || !out) return GDN_ERR_INVALID_ARG;
+  if (state_pool && (!cache_indices || s.pool < 1)) return GDN_ERR_INVALID_ARG;
+  for (const void* p : {q, k, v, (const void*)out, (const void*)state_pool})
+    if (!aligned16(p)) return GDN_ERR_INVALID_ARG;
+  if (!linear_prefill_grids_fit(s)) return GDN_ERR_UNSUPPORTED;
+  const size_t need = linear_workspace(s);
+  if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255) != 0))
+    return GDN_ERR_WORKSPACE;
+  const hipError_t e = launch_linear_prefill(s, q, k, v, log_decay, state_pool, cache_indices,
+                                             cu_seqlens, out, (char*)workspace,
+                                             (hipStream_t)stream);
+  return e == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+gdn_status_t gdn_linear_decode_fwd(const void* q, const void* k, const void* v,
+                                   const float* log_decay, float* state_pool,
+                                   const int64_t* cache_indices, void* out,
+                                   const gdn_linear_problem_t* prob, void* stream) {
+  LinearShape s;
+  const gdn_status_t ps = check_linear(prob, &s);
+  if (ps != GDN_OK) return ps;
+  if (s.N != s.B) return GDN_ERR_INVALID_ARG;  // exactly one token per request
+  if (s.B == 0) return GDN_OK;
+  if (!q || !k || !v || !log_decay || !state_pool || !cache_indices || !out || s.pool < 1)
+    return GDN_ERR_INVALID_ARG;
+  for (const void* p : {q, k, v, (const void*)out, (const void*)state_pool})
+    if (!aligned16(p)) return GDN_ERR_INVALID_ARG;
+  if (!linear_decode_grid_fits(s)) return GDN_ERR_UNSUPPORTED;
+  const hipError_t e = launch_linear_decode(s, q, k, v, log_decay, state_pool, cache_indices, out,
+                                            (hipStream_t)stream);
+  return e == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+size_t gdn_linear_bwd_workspace_size(const gdn_linear_problem_t* prob) {
+  LinearShape s;
+  return check_linear(prob, &s) == GDN_OK ? linear_bwd_workspace(s) : 0;
+}
+
+gdn_status_t gdn_linear_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                            const float* state_pool, const int64_t* cache_indices,
+                            const int64_t* cu_seqlens, const void* dout, const float* dstate,
+                            void* dq, void* dk, void* dv, float* dstate0,
+                            const gdn_linear_problem_t* prob, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  LinearShape s;
+  const gdn_status_t ps = check_linear(prob, &s);
+  if (ps != GDN_OK) return ps;
+  if (s.B == 0) return GDN_OK;
+  if (!log_decay || !cu_seqlens || (state_pool && (!cache_indices || s.pool < 1)))
+    return GDN_ERR_INVALID_ARG;
+  if (s.N > 0 && (!q || !k || !v || !dout || !dq || !dk || !dv)) return GDN_ERR_INVALID_ARG;
+  for (const void* p : {q, k, v, dout, (const void*)dq, (const void*)dk, (const void*)dv,
+                        (const void*)state_pool, (const void*)dstate, (const void*)dstate0})
+    if (!aligned16(p)) return GDN_ERR_INVALID_ARG;
+  if (!linear_bwd_grids_fit(s)) return GDN_ERR_UNSUPPORTED;
+  const size_t need = linear_bwd_workspace(s);
+  if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255) != 0))
+    return GDN_ERR_WORKSPACE;
+  const hipError_t e =
+      launch_linear_bwd(s, q, k, v, log_decay, state_pool, cache_indices, cu_seqlens, dout, dstate,
+                        dq, dk, dv, dstate0, (char*)workspace, (hipStream_t)stream);
+  return e == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+size_t gdn_adapter_workspace_size(const gdn_adapter_problem_t* prob) {
+  AdapterShape s;
+  return check_adapter(prob, &s) == GDN_OK ? adapter_workspace(s) : 0;
+}
+
+gdn_status_t gdn_adapter_fwd(const void* x, const void* base, const void* A, const void* B,
+                             const float* scaling, const int64_t* adapter_indices,
+                             const int64_t* cu_seqlens, void* out,
+                             const gdn_adapter_problem_t* prob, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  return run_adapter(x, base, A, B, scaling, adapter_indices, cu_seqlens, out, prob, false,
+                     workspace, workspace_bytes, stream);
+}
+
+gdn_status_t gdn_adapter_decode_fwd(const void* x, const void* base, const void* A, const void* B,
+                                    const float* scaling, const int64_t* adapter_indices,
+                                    void* out, const gdn_adapter_problem_t* prob, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  return run_adapter(x, base, A, B, scaling, adapter_indices, nullptr, out, prob, true, workspace,
+                     workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -465,6 +465,119 @@ gdn_status_t gdn_norm_bwd(const void* x, const float* weight, const float* bias,
                           const gdn_norm_problem_t* prob, void* workspace, size_t workspace_bytes,
                           void* stream);
 
+/* Shape of one call of linear attention (host struct). */
+typedef struct {
+  int64_t total_tokens; /* N                                                               */
+  int64_t batch;        /* B: requests                                                     */
+  int64_t pool_size;    /* slots in state_pool (ignored when state_pool is NULL)           */
+  int64_t q_stride;     /* elements between the tokens of q, at least num_qk_heads head_k  */
+  int64_t k_stride;     /* ... of k, likewise                                              */
+  int64_t v_stride;     /* ... of v, at least num_v_heads head_v                           */
+  int32_t num_qk_heads; /* H                                                               */
+  int32_t num_v_heads;  /* HV, a multiple of H: value head hv reads head hv / (HV / H)     */
+  int32_t head_k;       /* dk: 64, 128 or 256                                              */
+  int32_t head_v;       /* dv: 64, 128 or 256                                              */
+  int32_t dtype;        /* gdn_dtype_t of q, k, v, out, dout, dq, dk and dv                */
+  float scale;          /* c below, finite                                                 */
+  int32_t flags;        /* must be 0                                                       */
+  int32_t reserved;     /* must be 0                                                       */
+} gdn_linear_problem_t;
+
+/* Linear attention with a fixed decay for each head: the recurrence without gates or removal, on
+ * the packing and pool of gdn_prefill_fwd. For every request and value head, h = hv / (HV / H):
+ *   S <- e^{log_decay[hv]} S + v[t,hv] k[t,h]^T,     out[t,hv] = c S q[t,h]
+ *   q, k [N, H, dk] and v [N, HV, dv] in dtype, tokens q_stride, k_stride and v_stride apart
+ *        (slices of a projection's row; strides are whole multiples of 16 bytes)
+ *   log_decay [HV] fp32, not above 0 (an entry above 0 counts as 0): a constant of the model, it
+ *        has no gradient
+ *   state_pool [pool, HV, dv, dk] fp32, updated in place; NULL: zero start states, none kept (then
+ *        cache_indices is not read and may be NULL)
+ *   out [N, HV, dv] dense, dtype
+ * Evaluated in chunks on the matrix cores with fp32 sums: every factor keeps 24 bits in the
+ * states, and in the outputs of fp32 inputs; 16 bits in the outputs of bf16 inputs, which are then
+ * rounded to bf16, once. Long requests are worked on in pieces, whose length goes by N, B and the
+ * shape alone.
+ * A non-finite v also reaches that column of the up to 31 tokens before it in its request, and
+ * need not reach the states behind its piece once its decay there is zero in fp32. Every finite
+ * value is taken as it is; an infinite one may stand as NaN in whatever it reaches.
+ * q, k, v, out and state_pool 16-byte aligned. workspace: at least gdn_linear_workspace_size
+ * bytes, 256-byte aligned; its contents on entry do not matter. N == 0 or B == 0 is a no-op. */
+size_t gdn_linear_workspace_size(const gdn_linear_problem_t* prob);
+gdn_status_t gdn_linear_prefill_fwd(const void* q, const void* k, const void* v,
+                                    const float* log_decay, float* state_pool,
+                                    const int64_t* cache_indices, const int64_t* cu_seqlens,
+                                    void* out, const gdn_linear_problem_t* prob, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* One step: row b of q, k, v and out belongs to request b, N == B (GDN_ERR_INVALID_ARG
+ * otherwise), state_pool is required. No workspace. Arithmetic in fp32. */
+gdn_status_t gdn_linear_decode_fwd(const void* q, const void* k, const void* v,
+                                   const float* log_decay, float* state_pool,
+                                   const int64_t* cache_indices, void* out,
+                                   const gdn_linear_problem_t* prob, void* stream);
+
+/* Gradients of gdn_linear_prefill_fwd, for the scalar
+ *   L = <dout, out> + sum_b <dstate[b], request b's final state>.
+ *   state_pool: the pool as it was BEFORE the forward call (read only), or NULL as there
+ *   dout [N, HV, dv] dense, dtype; dstate [B, HV, dv, dk] fp32, or NULL for zero
+ *   dq, dk [N, H, dk], dv [N, HV, dv] dense, dtype: with D the gradient of the state behind a
+ *     token, D <- e^{log_decay} D + c dout q^T from the last token to the first,
+ *     dq = c S^T dout,  dk = D^T v,  dv = D k,  dq and dk summed over the value heads of a group
+ *   dstate0 [B, HV, dv, dk] fp32: gradient of each request's start state; NULL to skip
+ * All overwritten (dq, dk and dv on requests' rows). A request without tokens has dstate0 =
+ * dstate, a padding request zero. Precision as for the forward call: bf16 gradients are rounded
+ * once, dstate0 keeps 24 bits. All pointers but cu_seqlens and cache_indices 16-byte aligned.
+ * workspace: at least gdn_linear_bwd_workspace_size bytes, 256-byte aligned. */
+size_t gdn_linear_bwd_workspace_size(const gdn_linear_problem_t* prob);
+gdn_status_t gdn_linear_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                            const float* state_pool, const int64_t* cache_indices,
+                            const int64_t* cu_seqlens, const void* dout, const float* dstate,
+                            void* dq, void* dk, void* dv, float* dstate0,
+                            const gdn_linear_problem_t* prob, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Shape of one call of low-rank adapters (host struct). */
+typedef struct {
+  int64_t total_tokens; /* N                                                               */
+  int64_t batch;        /* B: requests                                                     */
+  int64_t x_stride;     /* elements between rows of x, at least `inputs`                   */
+  int64_t base_stride;  /* ... of base, at least `outputs`                                 */
+  int64_t out_stride;   /* ... of out, at least `outputs`                                  */
+  int32_t inputs;       /* K                                                               */
+  int32_t outputs;      /* M                                                               */
+  int32_t rank;         /* R: 1 to 128                                                     */
+  int32_t adapters;     /* in the bank, 0 to 4096                                          */
+  int32_t dtype;        /* gdn_dtype_t of x, base, A, B and out                            */
+  int32_t reserved;     /* must be 0                                                       */
+} gdn_adapter_problem_t;
+
+/* The low-rank adapters of a batch's requests beside a projection that they share: the projection
+ * (in front of gdn_conv_fwd, say) has formed base = x W^T for all rows, and for request b's rows
+ * with a = adapter_indices[b]
+ *   out = base + scaling[a] (x A[a]^T) B[a]^T,     out = base where a is outside [0, adapters)
+ *   x    [N, K], base and out [N, M], rows some stride apart; out may be base itself (the same
+ *        pointer and stride), and overlaps nothing otherwise
+ *   A    [adapters, R, K], B [adapters, M, R] dense; scaling [adapters] fp32
+ *   adapter_indices [B] int64: any number of requests may share an adapter
+ *   cu_seqlens [B + 1]
+ * fp32 sums; x A^T is held in fp32 and enters the second product with 16 bits (bf16) or 24 bits
+ * (fp32); the sum with base is rounded once. Vectors of 16 bytes where pointers, strides and sizes
+ * allow it, else element by element. Rows from cu_seqlens[B] on are not written.
+ * workspace: at least gdn_adapter_workspace_size bytes, 256-byte aligned. */
+size_t gdn_adapter_workspace_size(const gdn_adapter_problem_t* prob);
+gdn_status_t gdn_adapter_fwd(const void* x, const void* base, const void* A, const void* B,
+                             const float* scaling, const int64_t* adapter_indices,
+                             const int64_t* cu_seqlens, void* out,
+                             const gdn_adapter_problem_t* prob, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* gdn_adapter_fwd for one new token per request: row b belongs to request b, N == B
+ * (GDN_ERR_INVALID_ARG otherwise). */
+gdn_status_t gdn_adapter_decode_fwd(const void* x, const void* base, const void* A, const void* B,
+                                    const float* scaling, const int64_t* adapter_indices,
+                                    void* out, const gdn_adapter_problem_t* prob, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
 /* Debug check of the device-array preconditions: cu_seqlens[0] == 0, non-decreasing,
  * cu_seqlens[B] == N; cache_indices distinct and in [0, pool). Copies both arrays to
  * the host (16 bytes per request; at most 2^26 requests, GDN_ERR_UNSUPPORTED above that or
