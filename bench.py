@@ -85,8 +85,8 @@ DECODE_SOURCES = ("gdn_decode.hip", "gdn_internal.h")
 PROMOTE_SOURCES = ("gdn_promote.hip", "gdn_internal.h", "gdn_mfma.h")
 BACKWARD_SOURCES = ("gdn_backward.hip", "gdn_backward.h", "gdn_internal.h", "gdn_plan_gate.hip")
 LAYER_SOURCES = ("gdn_layer.h", "gdn_layer_api.hip", "gdn_conv.hip", "gdn_norm.hip",
-                 "gdn_ssm.hip", "gdn_ssm_scan.hip", "gdn_layer_linear.hip",
-                 "gdn_layer_adapter.hip")
+                 "gdn_ssm.hip", "gdn_ssm_scan.hip", "gdn_layer_chunk.h",
+                 "gdn_layer_linear.hip", "gdn_layer_linear_scan.hip", "gdn_layer_adapter.hip")
 PREFILL_F32_SOURCES = ("gdn_ref.hip", "gdn_plan_gate.hip", "gdn_api.hip", "gdn_internal.h",
                        "gdn_mfma.h")
 

@@ -197,7 +197,7 @@ struct LinearShape {
 size_t linear_workspace(const LinearShape& s);
 size_t linear_bwd_workspace(const LinearShape& s);
 bool linear_prefill_grids_fit(const LinearShape& s);
-bool linear_decode_grid_fits(const LinearShape& s);
+bool linear_token_grid_fits(const LinearShape& s);
 bool linear_bwd_grids_fit(const LinearShape& s);
 hipError_t launch_linear_prefill(const LinearShape& s, const void* q, const void* k, const void* v,
                                  const float* log_decay, float* state, const int64_t* idx,
@@ -205,6 +205,10 @@ hipError_t launch_linear_prefill(const LinearShape& s, const void* q, const void
 hipError_t launch_linear_decode(const LinearShape& s, const void* q, const void* k, const void* v,
                                 const float* log_decay, float* state, const int64_t* idx,
                                 void* out, hipStream_t st);
+// Requests of at most max_len tokens, token by token; the others are left alone.
+hipError_t launch_linear_short(const LinearShape& s, const void* q, const void* k, const void* v,
+                               const float* log_decay, float* state, const int64_t* idx,
+                               const int64_t* cu, void* out, int64_t max_len, hipStream_t st);
 hipError_t launch_linear_bwd(const LinearShape& s, const void* q, const void* k, const void* v,
                              const float* log_decay, const float* state, const int64_t* idx,
                              const int64_t* cu, const void* dout, const float* dstate, void* dq,

@@ -373,7 +373,7 @@ gdn_status_t gdn_linear_decode_fwd(const void* q, const void* k, const void* v,
     return GDN_ERR_INVALID_ARG;
   for (const void* p : {q, k, v, (const void*)out, (const void*)state_pool})
     if (!aligned16(p)) return GDN_ERR_INVALID_ARG;
-  if (!linear_decode_grid_fits(s)) return GDN_ERR_UNSUPPORTED;
+  if (!linear_token_grid_fits(s)) return GDN_ERR_UNSUPPORTED;
   const hipError_t e = launch_linear_decode(s, q, k, v, log_decay, state_pool, cache_indices, out,
                                             (hipStream_t)stream);
   return e == hipSuccess ? GDN_OK : GDN_ERR_HIP;

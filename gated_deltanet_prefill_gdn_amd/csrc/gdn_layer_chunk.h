@@ -1,0 +1,97 @@
+// Pieces shared by the chunked kernels of the layer operators (the selective scan and linear
+// attention): how requests are cut, bf16 parts of fp32 values, matrix operands out of LDS tiles,
+// chunks seen through buffer descriptors. Not part of the public C ABI.
+#pragma once
+
+#include "gdn_layer.h"
+#include "gdn_mfma.h"
+
+namespace gdn {
+namespace layer {
+
+using mfma::bf16x8_from_u32x4;
+using mfma::u32x2;
+using mfma::u32x4;
+typedef mfma::bf16x8 bfrag;
+typedef mfma::f32x4 acc4;
+
+// Pieces of a request of L tokens, and the tokens of one (a multiple of 64; the last piece may be
+// shorter): as equal as they come, at most lseg. An empty request counts one piece, which has
+// nothing to do.
+__device__ __forceinline__ int pieces_of(int64_t L64, int lseg, int& len) {
+  const int L = (int)L64;  // the call has less than 2^31 tokens
+  if (lseg == 0 || L64 <= lseg) {
+    len = L > 0 ? L : 0;
+    return 1;
+  }
+  const int n = (L + lseg - 1) / lseg;
+  len = ((L + n - 1) / n + 63) / 64 * 64;
+  return (L + len - 1) / len;
+}
+
+__device__ __forceinline__ int wave_inclusive(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int y = __shfl_up(v, off, 64);
+    if (lane >= off) v += y;
+  }
+  return v;
+}
+
+// 2^x in one instruction (one step off; results below 2^-126 are zero). The logs of the decays
+// are kept to base 2.
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// a and b as sums of P bf16 each, the parts of the two side by side in a register. No finite value
+// becomes infinite. Parts are rounded where the other factor is a sum as well (PAIRS), so that what
+// its products leave out, the second part times the third, is below 2^-24 and of either sign; where
+// the other factor is exact they are cut off, which takes fewer instructions: two parts are then
+// 2^-16 of a value off, three hold its 24 bits. (An infinite value leaves NaN in a later part.)
+template <int P, bool PAIRS>
+__device__ __forceinline__ void split(float a, float b, uint32_t (&part)[P]) {
+  static_assert(P > 1, "one part rounds, and may overflow");
+  constexpr float kTop = 0x1.FEp127f;  // the largest bf16
+#pragma unroll
+  for (int p = 0; p + 1 < P; ++p) {
+    if constexpr (PAIRS) {
+      const f32x2 v = p ? f32x2{a, b} : f32x2{__builtin_amdgcn_fmed3f(a, -kTop, kTop),
+                                              __builtin_amdgcn_fmed3f(b, -kTop, kTop)};
+      part[p] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+    } else {
+      part[p] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
+    }
+    a -= __uint_as_float(part[p] << 16);
+    b -= __uint_as_float(part[p] & 0xFFFF0000u);
+  }
+  part[P - 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+
+__device__ __forceinline__ bfrag bfrag_of(u32x2 lo, u32x2 hi) {
+  return bf16x8_from_u32x4(u32x4{lo[0], lo[1], hi[0], hi[1]});
+}
+// Eight entries of a row at k = kperm(g, 0..7), two 8-byte reads.
+__device__ __forceinline__ bfrag frag_kperm(const __bf16* row, int g) {
+  const u32x2 lo = *reinterpret_cast<const u32x2*>(row + 4 * g);
+  const u32x2 hi = *reinterpret_cast<const u32x2*>(row + 16 + 4 * g);
+  return bfrag_of(lo, hi);
+}
+// Column col0 + m of a row-major tile, rows 32 s + kperm(g, 0..7).
+__device__ __forceinline__ bfrag frag_col(const __bf16* tile, int ld, int col0, int s, int g,
+                                          int m) {
+  return bf16x8_from_u32x4(
+      mfma::col_frag_tr(reinterpret_cast<const uint16_t*>(tile), ld, col0, s, g, m));
+}
+
+// The rows of a chunk seen through a buffer descriptor: a lane's byte offset stays the same from
+// chunk to chunk, and rows behind the segment's end read as zero and drop what is stored to them
+// (the offset of such a row is at least (rows - 1) ld + cols, the descriptor's size).
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t chunk_rows(const void* base, int64_t ld_bytes, int rows,
+                                             int col_bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0,
+                                           (int)((rows - 1) * ld_bytes) + col_bytes, 0x00020000);
+}
+
+}  // namespace layer
+}  // namespace gdn

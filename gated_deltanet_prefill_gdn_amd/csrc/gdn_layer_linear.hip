@@ -1,11 +1,12 @@
-// Linear attention with a fixed decay for each head, token by token.
+// Linear attention token by token: one step for single tokens, and short requests of a prompt call,
+// where a chunk of 64 rows would be mostly padding.
 //
-// Every call is made of walks of one recurrence over the tokens of a request,
-//   W <- a W + w v k^T,   out = r W q,   a = e^{log_decay},
-// W (rows x DK, fp32) with the row of v: the forward call walks (q, k, v) over S; the gradients are
-// dq: (dout, v, k) over S^T, and from the last token to the first dv: (k, q, dout) over D and
-// dk: (v, dout, q) over D^T, D the gradient of the state. Row i of W depends on v[i] alone, so rows
-// are independent: a group of DK / 8 lanes holds one row, 8 fp32 per lane.
+//   S <- a S + v k^T,  out = c S q,   a = e^{log_decay}
+//
+// Row i of S (dv x dk, fp32) depends on v[i] alone, so rows are independent: a group of dk / 8
+// lanes holds one row, 8 fp32 per lane, and a workgroup covers kRowsPerBlock rows of one
+// (request, head). The state is read once, stays in registers over the request's tokens and is
+// written once. With one token per request (decode) the kernel is bound by the state's bytes.
 #include "gdn_layer.h"
 
 namespace gdn {
@@ -13,199 +14,160 @@ namespace layer {
 namespace {
 
 constexpr int kTokenThreads = 256;
+// Rows of a lane group: for one token two keep enough state loads in flight, with several tokens
+// four share each load of q and k.
+template <int DK, bool ONE>
+constexpr int kRows = ONE || DK == 64 ? 2 : 4;
+template <int DK, bool ONE>
+constexpr int kRowsPerBlock = (64 / (DK / 8)) * kRows<DK, ONE> * (kTokenThreads / 64);
+static_assert(kRowsPerBlock<64, false> == 64 && kRowsPerBlock<128, false> == 64 &&
+                  kRowsPerBlock<256, false> == 32 && kRowsPerBlock<64, true> == 64 &&
+                  kRowsPerBlock<128, true> == 32 && kRowsPerBlock<256, true> == 16,
+              "a workgroup's rows divide dv (64, 128 or 256)");
 
-struct Walk {
-  const void *q, *k, *v;
-  int64_t ldq, ldk, ldv;  // elements between tokens
-  int rq, rk, rv;         // value heads per head of q, k and v
-  void* out;              // [N, HV, rows] dense
-  const float* first;     // states in front of the walk, or NULL for zero
-  float* last;            // ... behind it, or NULL
-  bool first_pool, last_pool;  // by slot of the pool, else by request
-  int64_t row_step, col_step;  // of a state's entries
-  float read, write;
-  bool back;  // from the last token to the first; the decay comes behind a token
-};
-
-struct WalkArgs {
-  const float* log_decay;
-  const int64_t *idx, *cu;
-  int64_t N, npool;
-  int HV, rows;
-};
-
-__device__ __forceinline__ float decay_of(float g) {  // (NaN stays NaN)
-  return g > 0.f ? 1.f : expf(g);
+// x from another lane of the same 16-lane row, chosen by a DPP control code.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
 }
 
-template <int DK, typename T, typename TO>
-__global__ __launch_bounds__(kTokenThreads) void linear_walk_kernel(Walk w, WalkArgs a) {
-  constexpr int LPR = DK / 8, PER = kTokenThreads / LPR;
-  const int nrb = a.rows / PER;
-  const int64_t pair = blockIdx.x / (unsigned)nrb;
-  const int row = (int)(blockIdx.x - pair * nrb) * PER + threadIdx.x / LPR, gl = threadIdx.x % LPR;
-  const int64_t b = pair / a.HV;
-  const int hv = (int)(pair - b * a.HV);
-  int64_t t0 = b, t1 = b + 1;
-  if (a.cu) {
-    t0 = a.cu[b] < 0 ? 0 : a.cu[b];
-    t1 = a.cu[b + 1] < a.N ? a.cu[b + 1] : a.N;
+// Sum over an aligned group of LPR lanes, left in every lane of it.
+template <int LPR>
+__device__ __forceinline__ float group_sum(float x) {
+  static_assert(LPR == 8 || LPR == 16 || LPR == 32, "8 to 32 lanes per row");
+  x += dpp<0xB1>(x);   // lane ^ 1
+  x += dpp<0x4E>(x);   // lane ^ 2
+  x += dpp<0x141>(x);  // the other quad of the half-row, mirrored
+  if constexpr (LPR >= 16) x += dpp<0x140>(x);  // the other half of the row, mirrored
+  if constexpr (LPR >= 32) x += __shfl_xor(x, 16, 64);
+  return x;
+}
+
+// This lane's eight entries of a row of DK: 4 gl .. and DK / 2 + 4 gl .., so that a wave's load
+// covers contiguous half rows.
+template <int DK, typename T>
+__device__ __forceinline__ void load8(const T* row, int gl, float (&x)[8]) {
+  float lo[4], hi[4];
+  load_vec<4>(row + 4 * gl, lo);
+  load_vec<4>(row + DK / 2 + 4 * gl, hi);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = lo[i];
+    x[4 + i] = hi[i];
   }
-  const int64_t slot = a.idx ? a.idx[b] : b;
-  const bool live = !a.idx || (slot >= 0 && slot < a.npool);
-  const int64_t plane = (int64_t)a.rows * DK;
-  float s[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) s[e] = 0.f;
-  if (w.first && live) {
-    const float* p = w.first + ((w.first_pool ? slot : b) * a.HV + hv) * plane + row * w.row_step;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = p[(8 * gl + e) * w.col_step];
+}
+
+// ONE: one token per request, row b (cu is not read).
+template <int DK, typename T, bool ONE>
+__global__ __launch_bounds__(kTokenThreads) void linear_token_kernel(
+    LinearShape s, const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+    const float* __restrict__ log_decay, float* __restrict__ state_pool,
+    const int64_t* __restrict__ idx, const int64_t* __restrict__ cu, T* __restrict__ out, int nrb,
+    int64_t max_len) {
+  constexpr int LPR = DK / 8, RPW = 64 / LPR, NR = kRows<DK, ONE>, RWV = RPW * NR;
+  const uint32_t pair = blockIdx.x / (uint32_t)nrb;
+  const int rb = (int)(blockIdx.x - pair * (uint32_t)nrb);
+  const uint32_t b = pair / (uint32_t)s.HV;
+  const int hv = (int)(pair - b * (uint32_t)s.HV), h = hv / (s.HV / s.H);
+  int64_t t = b, t_end = (int64_t)b + 1;
+  if constexpr (!ONE) {
+    t = cu[b] < 0 ? 0 : cu[b];
+    t_end = cu[b + 1] < s.N ? cu[b + 1] : s.N;
   }
-  const float decay = decay_of(a.log_decay[hv]);
-  const int64_t n = live && t1 > t0 ? t1 - t0 : 0;
-  for (int64_t i = 0; i < n; ++i) {
-    const int64_t t = w.back ? t1 - 1 - i : t0 + i;
-    const T* const q = reinterpret_cast<const T*>(w.q) + t * w.ldq + (hv / w.rq) * DK + 8 * gl;
-    const T* const k = reinterpret_cast<const T*>(w.k) + t * w.ldk + (hv / w.rk) * DK + 8 * gl;
-    const float v =
-        w.write * (float)reinterpret_cast<const T*>(w.v)[t * w.ldv + (int64_t)(hv / w.rv) * a.rows + row];
-    const float before = w.back ? 1.f : decay;
-    float o = 0.f;
+  const int64_t slot = state_pool ? idx[b] : 0;
+  if (t >= t_end || t_end - t > max_len || (state_pool && (slot < 0 || slot >= s.pool))) return;
+  const int l = threadIdx.x & 63, gl = l % LPR;
+  const int r0 = rb * kRowsPerBlock<DK, ONE> + (threadIdx.x >> 6) * RWV + l / LPR;
+  float* const sp = state_pool + ((slot * s.HV + hv) * (int64_t)s.dv + r0) * DK + 4 * gl;
+  f32x4 st[NR][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      s[e] = __builtin_fmaf(before, s[e], v * (float)k[e]);
-      o = __builtin_fmaf(s[e], (float)q[e], o);
+  for (int j = 0; j < NR; ++j)
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+      st[j][half] = ONE || state_pool
+                        ? __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(
+                              sp + j * RPW * DK + half * (DK / 2)))
+                        : f32x4{0.f, 0.f, 0.f, 0.f};
+  const float g = log_decay[hv], a = g > 0.f ? 1.f : expf(g);
+  for (; t < t_end; ++t) {
+    float kk[8], qq[8], vr[NR];
+    load8<DK>(k + t * s.ldk + h * DK, gl, kk);
+    load8<DK>(q + t * s.ldq + h * DK, gl, qq);
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+      vr[j] = (float)v[t * s.ldv + (int64_t)hv * s.dv + r0 + j * RPW];
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+      float o = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float se = __builtin_fmaf(a, st[j][e / 4][e % 4], vr[j] * kk[e]);
+        st[j][e / 4][e % 4] = se;
+        o = __builtin_fmaf(se, qq[e], o);
+      }
+      o = group_sum<LPR>(o);
+      if (gl == 0) out[(t * s.HV + hv) * s.dv + r0 + j * RPW] = (T)(s.scale * o);
     }
+  }
+  if (!ONE && !state_pool) return;
 #pragma unroll
-    for (int off = 1; off < LPR; off <<= 1) o += __shfl_xor(o, off, 64);
-    if (gl == 0) reinterpret_cast<TO*>(w.out)[(t * a.HV + hv) * a.rows + row] = (TO)(w.read * o);
-    if (w.back)
+  for (int j = 0; j < NR; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] *= decay;
-  }
-  if (w.last && (live || !w.last_pool)) {
-    float* p = w.last + ((w.last_pool ? slot : b) * a.HV + hv) * plane + row * w.row_step;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) p[(8 * gl + e) * w.col_step] = s[e];
-  }
+    for (int half = 0; half < 2; ++half)
+      __builtin_nontemporal_store(
+          st[j][half], reinterpret_cast<f32x4*>(sp + j * RPW * DK + half * (DK / 2)));
 }
 
-// dq and dk of a group's head: the sum over its value heads, in order.
-template <typename T>
-__global__ __launch_bounds__(256) void linear_group_sum_kernel(const float* part, T* out,
-                                                               const int64_t* idx,
-                                                               const int64_t* cu, int64_t B,
-                                                               int64_t N, int64_t npool, int H,
-                                                               int rep, int d) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= N * H * d) return;
-  const int64_t t = i / ((int64_t)H * d);
-  if (t < cu[0] || t >= cu[B]) return;
-  if (idx) {
-    const int64_t slot = idx[request_of(cu, B, t)];
-    if (slot < 0 || slot >= npool) return;
+int rows_per_block(int dk, bool one) {
+  return dk == 256 ? (one ? kRowsPerBlock<256, true> : kRowsPerBlock<256, false>)
+         : dk == 128 ? (one ? kRowsPerBlock<128, true> : kRowsPerBlock<128, false>)
+                     : kRowsPerBlock<64, true>;
+}
+
+int64_t token_blocks(const LinearShape& s, bool one) {
+  return s.B * s.HV * (s.dv / rows_per_block(s.dk, one));
+}
+
+template <bool ONE>
+hipError_t launch_token(const LinearShape& s, const void* q, const void* k, const void* v,
+                        const float* log_decay, float* state, const int64_t* idx,
+                        const int64_t* cu, void* out, int64_t max_len, hipStream_t st) {
+  const dim3 grid((unsigned)token_blocks(s, ONE)), threads(kTokenThreads);
+  const int nrb = s.dv / rows_per_block(s.dk, ONE);
+#define GDN_LINEAR_CASE(DK, T)                                                                  \
+  if (s.dk == DK && s.bf16 == (sizeof(T) == 2)) {                                               \
+    hipLaunchKernelGGL((linear_token_kernel<DK, T, ONE>), grid, threads, 0, st, s, (const T*)q, \
+                       (const T*)k, (const T*)v, log_decay, state, idx, cu, (T*)out, nrb,       \
+                       max_len);                                                                \
+    return hipGetLastError();                                                                   \
   }
-  const int64_t th = i / d;
-  float s = 0.f;
-  for (int r = 0; r < rep; ++r) s += part[(th * rep + r) * d + (i - th * d)];
-  out[i] = (T)s;
-}
-
-template <typename T, typename TO>
-hipError_t launch_walk(const Walk& w, const WalkArgs& a, int64_t B, int DK, hipStream_t st) {
-  const int64_t blocks = B * a.HV * (a.rows / (kTokenThreads / (DK / 8)));
-  const auto kernel = DK == 64    ? linear_walk_kernel<64, T, TO>
-                      : DK == 128 ? linear_walk_kernel<128, T, TO>
-                                  : linear_walk_kernel<256, T, TO>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kTokenThreads), 0, st, w, a);
-  return hipGetLastError();
-}
-
-template <typename T>
-hipError_t forward(const LinearShape& s, const void* q, const void* k, const void* v,
-                   const float* log_decay, float* state, const int64_t* idx, const int64_t* cu,
-                   void* out, hipStream_t st) {
-  const int rep = s.HV / s.H;
-  const Walk w{q, k, v, s.ldq, s.ldk, s.ldv, rep, rep, 1, out, state, state, true, true,
-               s.dk, 1, s.scale, 1.f, false};
-  const WalkArgs a{log_decay, state ? idx : nullptr, cu, s.N, s.pool, s.HV, s.dv};
-  return launch_walk<T, T>(w, a, s.B, s.dk, st);
-}
-
-template <typename T>
-hipError_t backward(const LinearShape& s, const void* q, const void* k, const void* v,
-                    const float* log_decay, const float* state, const int64_t* idx,
-                    const int64_t* cu, const void* dout, const float* dstate, void* dq, void* dk,
-                    void* dv, float* dstate0, float* ws, hipStream_t st) {
-  const int rep = s.HV / s.H;
-  const int64_t ldo = (int64_t)s.HV * s.dv, part = s.N * s.HV * s.dk;
-  const WalkArgs ak{log_decay, state ? idx : nullptr, cu, s.N, s.pool, s.HV, s.dk};
-  const WalkArgs av{log_decay, state ? idx : nullptr, cu, s.N, s.pool, s.HV, s.dv};
-  const Walk wq{dout, v, k, ldo, s.ldv, s.ldk, 1, 1, rep, rep > 1 ? ws : dq, state, nullptr, true,
-                false, 1, s.dk, s.scale, 1.f, false};
-  const Walk wk{v, dout, q, s.ldv, ldo, s.ldq, 1, 1, rep, rep > 1 ? ws + part : dk, dstate,
-                nullptr, false, false, 1, s.dk, 1.f, s.scale, true};
-  const Walk wv{k, q, dout, s.ldk, s.ldq, ldo, rep, rep, 1, dv, dstate, dstate0, false, false,
-                s.dk, 1, 1.f, s.scale, true};
-  hipError_t e;
-  if (rep == 1) {
-    if ((e = launch_walk<T, T>(wq, ak, s.B, s.dv, st)) != hipSuccess) return e;
-    if ((e = launch_walk<T, T>(wk, ak, s.B, s.dv, st)) != hipSuccess) return e;
-    return launch_walk<T, T>(wv, av, s.B, s.dk, st);
-  }
-  if ((e = launch_walk<T, float>(wq, ak, s.B, s.dv, st)) != hipSuccess) return e;
-  if ((e = launch_walk<T, float>(wk, ak, s.B, s.dv, st)) != hipSuccess) return e;
-  if ((e = launch_walk<T, T>(wv, av, s.B, s.dk, st)) != hipSuccess) return e;
-  const int64_t n = s.N * s.H * s.dk;
-  if (n == 0) return hipSuccess;
-  for (int i = 0; i < 2; ++i) {
-    hipLaunchKernelGGL(linear_group_sum_kernel<T>, dim3((unsigned)cdiv(n, 256)), dim3(256), 0, st,
-                       ws + i * part, (T*)(i ? dk : dq), state ? idx : nullptr, cu, s.B, s.N,
-                       s.pool, s.H, rep, s.dk);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  return hipSuccess;
-}
-
-bool walk_grid_fits(const LinearShape& s, int DK, int rows) {
-  return grid_ok(s.B * s.HV * (rows / (kTokenThreads / (DK / 8))), kTokenThreads);
+  GDN_LINEAR_CASE(64, __bf16)
+  GDN_LINEAR_CASE(128, __bf16)
+  GDN_LINEAR_CASE(256, __bf16)
+  GDN_LINEAR_CASE(64, float)
+  GDN_LINEAR_CASE(128, float)
+  GDN_LINEAR_CASE(256, float)
+#undef GDN_LINEAR_CASE
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t linear_workspace(const LinearShape&) { return 0; }
-size_t linear_bwd_workspace(const LinearShape& s) {
-  return s.HV > s.H ? align256(2 * sizeof(float) * s.N * s.HV * s.dk) : 0;
-}
-bool linear_prefill_grids_fit(const LinearShape& s) { return walk_grid_fits(s, s.dk, s.dv); }
-bool linear_decode_grid_fits(const LinearShape& s) { return walk_grid_fits(s, s.dk, s.dv); }
-bool linear_bwd_grids_fit(const LinearShape& s) {
-  return walk_grid_fits(s, s.dk, s.dv) && walk_grid_fits(s, s.dv, s.dk) &&
-         grid_ok(cdiv(s.N * s.H * s.dk, 256), 256);
-}
-
-hipError_t launch_linear_prefill(const LinearShape& s, const void* q, const void* k, const void* v,
-                                 const float* log_decay, float* state, const int64_t* idx,
-                                 const int64_t* cu, void* out, char*, hipStream_t st) {
-  return s.bf16 ? forward<__bf16>(s, q, k, v, log_decay, state, idx, cu, out, st)
-                : forward<float>(s, q, k, v, log_decay, state, idx, cu, out, st);
+bool linear_token_grid_fits(const LinearShape& s) {
+  return grid_ok(token_blocks(s, true), kTokenThreads);  // the larger of the two grids
 }
 
 hipError_t launch_linear_decode(const LinearShape& s, const void* q, const void* k, const void* v,
                                 const float* log_decay, float* state, const int64_t* idx,
                                 void* out, hipStream_t st) {
-  return launch_linear_prefill(s, q, k, v, log_decay, state, idx, nullptr, out, nullptr, st);
+  return launch_token<true>(s, q, k, v, log_decay, state, idx, nullptr, out, 1, st);
 }
 
-hipError_t launch_linear_bwd(const LinearShape& s, const void* q, const void* k, const void* v,
-                             const float* log_decay, const float* state, const int64_t* idx,
-                             const int64_t* cu, const void* dout, const float* dstate, void* dq,
-                             void* dk, void* dv, float* dstate0, char* ws, hipStream_t st) {
-  return s.bf16 ? backward<__bf16>(s, q, k, v, log_decay, state, idx, cu, dout, dstate, dq, dk, dv,
-                                   dstate0, (float*)ws, st)
-                : backward<float>(s, q, k, v, log_decay, state, idx, cu, dout, dstate, dq, dk, dv,
-                                  dstate0, (float*)ws, st);
+hipError_t launch_linear_short(const LinearShape& s, const void* q, const void* k, const void* v,
+                               const float* log_decay, float* state, const int64_t* idx,
+                               const int64_t* cu, void* out, int64_t max_len, hipStream_t st) {
+  return launch_token<false>(s, q, k, v, log_decay, state, idx, cu, out, max_len, st);
 }
 
 }  // namespace layer

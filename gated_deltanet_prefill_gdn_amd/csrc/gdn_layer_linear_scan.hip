@@ -1,0 +1,890 @@
+// Linear attention with a fixed decay for each head, chunk by chunk on the matrix cores: prompts and
+// gradients.
+//
+// Every call is made of walks of one recurrence over the tokens of a request,
+//   W <- a W + w v k^T,   out = r W q,   a = e^{log_decay},
+// W (rows x DK, fp32) with the row of v. The forward call walks (q, k, v) over S. The gradients are
+// three walks: dq with (dout, v, k) over S^T, and from the last token to the first dv with
+// (k, q, dout) over D and dk with (v, dout, q) over D^T, D the gradient of the state behind a token;
+// there the decay comes behind a token's read instead of in front of its write. A chunk of n rows
+// (i = 0 .. n - 1 in the order of the walk; b = 1 for walks backwards, else 0) is four products:
+//   out_i = r a^{i + 1 - b} W q_i + sum_{j <= i} r w a^{i - j} (q_i . k_j) v_j
+//   W    <- a^n W + sum_j (w a^{n - 1 - j + b} v_j) k_j^T
+// all in 16x16x32 matrix instructions with fp32 sums. The decays depend on differences of rows
+// alone: a lane keeps those of a tile on the diagonal and of one beside it in registers.
+//
+// A workgroup of four waves walks the chunks of one segment of a request for one head and 64 or 128 of W's rows,
+// a quarter of them each, which stay in registers (as columns of W^T) from the first chunk to the last. In
+// the D layout of the products a lane holds four consecutive entries of one column, which is also
+// what the next products want as an operand, so the state and the scores never move between lanes.
+//
+// Requests longer than a segment are cut into equal pieces: a first launch forms each piece's state
+// from zero (of S, and for gradients of D; their transposes are the same memory), a second joins
+// them in order into the pieces' start states and the final one, and a third forms the outputs of
+// all pieces side by side and takes the requests that are not cut from start to end. A piece's state
+// is summed from its end, and only as far back as weights are not zero in fp32: heads that forget
+// fast stop after a few chunks.
+//
+// Precision: bf16 inputs enter the products as they are. The decayed v of the state's update are
+// three bf16 (24 bits), since states are fp32 results. What only outputs take, which end as bf16, is
+// two bf16 (16 bits): the decayed scores, the state that W q reads, and the decayed v where a piece's
+// state is only formed to be read so. For fp32 inputs every operand is three bf16 and a product takes
+// the six pairs of parts that reach 2^-24. Powers of the decay come from products in fp64, so that
+// they are a step or two of fp32 off however far they reach.
+#include "gdn_layer_chunk.h"
+
+namespace gdn {
+namespace layer {
+namespace {
+
+using mfma::kperm;
+using mfma::mma_bf16;
+
+struct Walk {
+  const void *q, *k, *v;
+  int64_t ldq, ldk, ldv;  // elements between tokens
+  int rq, rk, rv;         // value heads per head of q, k and v
+  void* out;              // [N, HV, rows] dense; in the states' pass the pieces' states
+  const float* first;     // states in front of the walk, NULL: zero
+  float* last;            // ... behind it, NULL: not wanted
+  float* pieces;          // states of the pieces of cut requests: [places][HV][rows][DK]
+  int first_pool, last_pool;  // by slot of the pool, else by request
+  int transposed;         // states lie in memory as [DK][rows]
+  int back;               // from the last token to the first
+  float read, write;
+};
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kWalks = 3;
+struct ScanArgs {
+  Walk walk[kWalks];
+  const float* log_decay;
+  const int64_t *idx, *cu;  // idx NULL: every request is live
+  int64_t N, nreq, npool;
+  int walks, HV, rep, rows;
+  int col_blocks;  // of a head's rows
+  int lseg;        // tokens of a segment (a multiple of 64), 0: nothing is cut
+  int max_cut;     // places for pieces' states
+  int short_len;   // requests of at most this many tokens are left to the token kernel
+};
+
+__device__ __forceinline__ int64_t begin_of(const ScanArgs& a, int64_t b) {
+  return a.cu[b] < 0 ? 0 : a.cu[b];
+}
+__device__ __forceinline__ int64_t end_of(const ScanArgs& a, int64_t b) {
+  return a.cu[b + 1] < a.N ? a.cu[b + 1] : a.N;
+}
+__device__ __forceinline__ int64_t slot_of(const ScanArgs& a, int64_t b) {
+  return a.idx ? a.idx[b] : b;
+}
+__device__ __forceinline__ bool live_slot(const ScanArgs& a, int64_t slot) {
+  return !a.idx || (slot >= 0 && slot < a.npool);
+}
+
+struct Segment {
+  int64_t req, slot;
+  int64_t t0, t1;  // tokens
+  int count;       // segments of its request
+  int place;       // among the pieces of cut requests (cut requests only)
+};
+
+// Segment number `seg` of the call, by a scan over the requests, 64 at a time in every wave.
+__device__ __forceinline__ bool find_segment(const ScanArgs& a, int seg, Segment& s) {
+  const int lane = threadIdx.x & 63;
+  int len = 0, index = 0;
+  s.count = 1;
+  s.place = 0;
+  if (a.lseg == 0) {
+    s.req = seg;
+    if (seg >= a.nreq) return false;
+  } else {
+    int before = 0, before_cut = 0;
+    bool found = false;
+    for (int64_t base = 0; base < a.nreq; base += 64) {
+      const int64_t b = base + lane;
+      int mine = 0;
+      const int n = b < a.nreq ? pieces_of(end_of(a, b) - begin_of(a, b), a.lseg, mine) : 0;
+      const int inc = wave_inclusive(n), cut = wave_inclusive(n > 1 ? n : 0);
+      const uint64_t over = __ballot(before + inc > seg);
+      if (over) {
+        const int k = __builtin_ctzll(over);
+        s.count = __builtin_amdgcn_readlane(n, k);
+        index = seg - before - (__builtin_amdgcn_readlane(inc, k) - s.count);
+        s.place = before_cut + __builtin_amdgcn_readlane(cut, k) - s.count + index;
+        s.req = base + k;
+        len = __builtin_amdgcn_readlane(mine, k);
+        found = true;
+        break;
+      }
+      before += __builtin_amdgcn_readlane(inc, 63);
+      before_cut += __builtin_amdgcn_readlane(cut, 63);
+    }
+    if (!found) return false;
+  }
+  const int64_t begin = begin_of(a, s.req), end = end_of(a, s.req);
+  s.t0 = begin + (int64_t)index * len;
+  s.t1 = index + 1 < s.count ? s.t0 + len : end;
+  s.slot = slot_of(a, s.req);
+  if (s.count > 1 && s.place >= a.max_cut) return false;  // cu_seqlens breaks its precondition
+  return s.t0 < s.t1 && end - begin > a.short_len && live_slot(a, s.slot);
+}
+
+// log2 of a head's decay: not above 0, finite (2^-1e30 is zero as any lower power), NaN stays NaN.
+__device__ __forceinline__ double log2_decay(float g) {
+  const double x = (double)g * 1.4426950408889634;
+  return x > 0. ? 0. : x < -1e30 ? -1e30 : x;
+}
+// a^n from log2 a: the exponent's whole part scales a power of its fraction.
+__device__ __forceinline__ float power(double g2, int64_t n) {
+  const double p = g2 * (double)n;
+  if (p < -200.) return 0.f;
+  const double whole = __builtin_rint(p);
+  return __builtin_amdgcn_ldexpf(exp2_((float)(p - whole)), (int)whole);
+}
+
+// Staging of a tile of CH rows x COLS entries: 16-byte pieces in registers between the load and
+// the LDS store, so that the next chunk's rows travel while this one is worked on. Walks backwards
+// take the rows in reverse order.
+template <typename T, int CH, int COLS>
+struct Stage {
+  static constexpr int V = 16 / (int)sizeof(T);
+  static constexpr int PER_ROW = COLS / V, PIECES = CH * PER_ROW / kThreads;
+  static constexpr int ROWS = kThreads / PER_ROW;  // rows of one piece of all threads
+  static_assert(CH * PER_ROW % kThreads == 0 && kThreads % PER_ROW == 0, "whole rows at a time");
+  u32x4 r[PIECES];
+  __device__ __forceinline__ void load(const T* base, int64_t ld, int rows, bool back) {
+    const int ldb = (int)ld * (int)sizeof(T), row = (int)threadIdx.x / PER_ROW;
+    const rsrc_t q = chunk_rows(base, ldb, rows, COLS * (int)sizeof(T));
+    // (a row in front of the tile has an offset below zero, beyond every size as an unsigned one)
+    const int at = (back ? rows - 1 - row : row) * ldb + (int)(threadIdx.x % PER_ROW) * 16;
+    const int step = back ? -ROWS * ldb : ROWS * ldb;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+      r[i] = __builtin_bit_cast(u32x4,
+                                __builtin_amdgcn_raw_buffer_load_b128(q, at + i * step, 0, 0));
+  }
+  // as NP tiles of bf16 parts, `plane` entries apart
+  template <int NP, bool WIDE>
+  __device__ __forceinline__ void store(__bf16* to, int plane, int ld) const {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const int p = i * kThreads + threadIdx.x, row = p / PER_ROW, c = p % PER_ROW * V;
+      if constexpr (NP == 1) {
+        if constexpr (WIDE) {
+          *reinterpret_cast<u32x4*>(to + row * ld + c) = r[i];
+        } else {  // rows start on 8 bytes
+          u32x2* const q = reinterpret_cast<u32x2*>(to + row * ld + c);
+          q[0] = u32x2{r[i][0], r[i][1]};
+          q[1] = u32x2{r[i][2], r[i][3]};
+        }
+      } else {
+        const f32x4 v = __builtin_bit_cast(f32x4, r[i]);
+        uint32_t lo[NP], hi[NP];
+        split<NP, true>(v[0], v[1], lo);
+        split<NP, true>(v[2], v[3], hi);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          *reinterpret_cast<u32x2*>(to + p * plane + row * ld + c) = u32x2{lo[p], hi[p]};
+      }
+    }
+  }
+};
+
+// The tiles of the lower triangle of NT x NT tiles (row tt, column jt), dealt to the waves so that
+// most of a wave's tiles are of one row: three in rows 3 and 2, (1, 0), (1, 1) and (3, 3), (0, 0);
+// of 32 rows (0, 0), (1, 0) and (1, 1).
+template <int NT>
+__device__ __forceinline__ bool deal(int wave, int i, int& tt, int& jt) {
+  if constexpr (NT == 4) {
+    tt = 3 - wave;
+    jt = i;
+    if (wave == 2 && i == 2) tt = jt = 3;
+    return wave < 3 || i == 0;
+  } else {
+    tt = wave > 0;
+    jt = wave > 1;
+    return wave < 3;
+  }
+}
+
+// What a workgroup does with its segment: a whole request, outputs and state; the state of a
+// piece from zero; the outputs of a piece from its start state.
+enum Mode { kWhole, kState, kOutput };
+
+template <typename T, int DK, int CH, int COLS>
+struct Dims {
+  static constexpr int PT = COLS / 64;  // tiles of 16 of W's rows a wave
+  static constexpr int NP = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of an input
+  static constexpr int PS = sizeof(T) == 4 ? 3 : 2;  // ... of the decayed scores and of W in W q
+  // LDS rows. q is read in 8-byte pieces down 16 rows: fewest conflicts where the stride is 2 mod
+  // 4 words. k and v are read transposed and in 16-byte pieces: none where it is 8 mod 16 words.
+  static constexpr int LDQ = DK + 12, LDK = DK + 16, LDV = COLS + 16, LDP = CH + 8;
+  static constexpr int TileQ = CH * LDQ, TileK = CH * LDK, TileV = CH * LDV, TileP = CH * LDP;
+  static constexpr int AtV = NP * TileK * 2, AtW = AtV + NP * TileV * 2;
+  static constexpr int AtQ = AtW + 2 * CH * 4, AtP = AtQ + NP * TileQ * 2;
+  static constexpr int Bytes = AtP + PS * TileP * 2;
+  static_assert(AtV % 16 == 0 && AtW % 16 == 0 && AtQ % 16 == 0 && AtP % 16 == 0, "16-byte rows");
+};
+
+template <typename T, typename TO, int DK, int CH, int COLS, Mode MODE>
+__device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, const Segment& sg,
+                                             int hv, int col0, char* lds) {
+  using D = Dims<T, DK, CH, COLS>;
+  constexpr bool F32 = sizeof(T) == 4, OUT = MODE != kState;
+  constexpr int NP = D::NP, PS = D::PS, PT = D::PT;
+  // ... of the update's decayed v: the state of a piece's outputs is only read by W q
+  constexpr int NU = MODE == kOutput ? PS : 3;
+  constexpr int NT = CH / 16, NK = CH / 32;    // token tiles, k steps over tokens
+  constexpr int NS = DK / 16, NKS = DK / 32;   // state tiles, k steps over state entries
+  constexpr int TRI = NT == 4 ? 3 : 1;         // tiles of scores for a wave at most
+  constexpr int LDQ = D::LDQ, LDK = D::LDK, LDV = D::LDV, LDP = D::LDP;
+  __bf16* const s_k = reinterpret_cast<__bf16*>(lds);
+  __bf16* const s_v = reinterpret_cast<__bf16*>(lds + D::AtV);
+  float* const s_w = reinterpret_cast<float*>(lds + D::AtW);
+  __bf16* const s_q = reinterpret_cast<__bf16*>(lds + D::AtQ);
+  // decayed scores, row i; entry 32 k + 8 g + e is row j = 32 k + kperm(g, e)
+  __bf16* const s_p = reinterpret_cast<__bf16*>(lds + D::AtP);
+
+  const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int p0 = col0 + 16 * PT * wv;  // the wave's rows of W
+  const bool back = w.back != 0;
+  const int rows_all = a.rows;
+
+  const T* const gq = reinterpret_cast<const T*>(w.q) + (int64_t)(hv / w.rq) * DK;
+  const T* const gk = reinterpret_cast<const T*>(w.k) + (int64_t)(hv / w.rk) * DK;
+  const T* const gv = reinterpret_cast<const T*>(w.v) + (int64_t)(hv / w.rv) * rows_all + col0;
+  TO* const gout = reinterpret_cast<TO*>(w.out) + (int64_t)hv * rows_all + p0;
+  const int64_t ldo = (int64_t)a.HV * rows_all, plane = (int64_t)rows_all * DK;
+
+  // W^T: st[s tile][column tile], entries 16 s + 4 g .. + 3 of column p0 + 16 pt + r
+  acc4 st[NS][PT];
+  const float* from = nullptr;
+  if constexpr (MODE == kOutput)
+    from = w.pieces + ((int64_t)sg.place * a.HV + hv) * plane;
+  else if constexpr (MODE == kWhole)
+    from = w.first ? w.first + ((w.first_pool ? sg.slot : sg.req) * a.HV + hv) * plane : nullptr;
+  if (from == nullptr) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) st[s][pt] = acc4{0.f, 0.f, 0.f, 0.f};
+  } else if (w.transposed) {
+    from += (int64_t)(4 * g) * rows_all + p0 + r;
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          st[s][pt][e] = from[(int64_t)(16 * s + e) * rows_all + 16 * pt];
+  } else {
+    from += (int64_t)(p0 + r) * DK + 4 * g;
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+        st[s][pt] = *reinterpret_cast<const acc4*>(from + 16 * pt * DK + 16 * s);
+  }
+
+  Stage<T, CH, DK> qk, qq;  // the next chunk's rows
+  Stage<T, CH, COLS> qv;
+  const int len = (int)(sg.t1 - sg.t0), chunks = (len + CH - 1) / CH;
+  // Chunks in the order of the walk; a piece's state alone is summed from the walk's end.
+  auto place = [&](int n) { return (OUT ? n : chunks - 1 - n) * CH; };
+  auto rows_at = [&](int i0) { return len - i0 < CH ? len - i0 : CH; };
+  auto token_at = [&](int i0) {  // the lowest of the chunk
+    return back ? sg.t1 - i0 - rows_at(i0) : sg.t0 + i0;
+  };
+  auto fetch = [&](int i0) {
+    const int rows = rows_at(i0);
+    const int64_t t = token_at(i0);
+    qk.load(gk + t * w.ldk, w.ldk, rows, back);
+    if constexpr (OUT) qq.load(gq + t * w.ldq, w.ldq, rows, back);
+    qv.load(gv + t * w.ldv, w.ldv, rows, back);
+  };
+  fetch(place(0));
+
+  // Decays. Scores: row r of a tile against its columns 4 g + e, on the diagonal and one tile off.
+  const double g2 = log2_decay(a.log_decay[hv]);
+  const int nlast = len - (chunks - 1) * CH;
+  float on[4], off[4], reach[NT];
+  const float a16 = power(g2, 16), a32 = power(g2, 32);
+  if constexpr (OUT) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int lag = r - (4 * g + e);
+      on[e] = w.read * w.write * power(g2, lag > 0 ? lag : 0);
+      off[e] = w.read * w.write * power(g2, 16 + lag);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) reach[t] = w.read * power(g2, 16 * t + r + 1 - w.back);
+  }
+  // weights in the state's update, of a full chunk and of the last
+  if (tid < CH) {
+    s_w[tid] = w.write * power(g2, CH - 1 - tid + w.back);
+    s_w[CH + tid] = tid < nlast ? w.write * power(g2, nlast - 1 - tid + w.back) : 0.f;
+  }
+  const float a_full = power(g2, CH), a_last = power(g2, nlast);
+
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    const int i0 = place(chunk), rows = rows_at(i0);
+    const int64_t t0 = token_at(i0);
+    if (chunk > 0) __syncthreads();  // the chunk before has been read
+    qk.template store<NP, true>(s_k, D::TileK, LDK);
+    if constexpr (OUT) qq.template store<NP, false>(s_q, D::TileQ, LDQ);
+    qv.template store<NP, true>(s_v, D::TileV, LDV);
+    __syncthreads();
+    if (chunk + 1 < chunks) fetch(place(chunk + 1));
+
+    acc4 y[NT][PT];  // out^T: columns 16 pt + 4 g .. + 3 of row 16 t + r
+    if constexpr (OUT) {
+      // scores^T, j x i: each wave some of the tiles, decayed
+#pragma unroll
+      for (int i = 0; i < TRI; ++i) {
+        int tt, jt;
+        if (!deal<NT>(wv, i, tt, jt)) break;
+        acc4 half[2] = {acc4{0.f, 0.f, 0.f, 0.f}, acc4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int k = 0; k < NKS; ++k)
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            const u32x2* const qp = reinterpret_cast<const u32x2*>(
+                s_q + p * D::TileQ + (16 * tt + r) * LDQ + 32 * k + 8 * g);
+            const bfrag q = bfrag_of(qp[0], qp[1]);
+#pragma unroll
+            for (int o = 0; o + p < NP; ++o)
+              half[k % 2] =
+                  mma_bf16(*reinterpret_cast<const bfrag*>(s_k + o * D::TileK +
+                                                           (16 * jt + r) * LDK + 32 * k + 8 * g),
+                           q, half[k % 2]);
+          }
+        const acc4 sc = half[0] + half[1];
+        __bf16* const to = s_p + (16 * tt + r) * LDP + 32 * (jt / 2) + 8 * g + 4 * (jt % 2);
+        float v[4];
+        if (jt < tt) {
+          const float far = tt - jt == 1 ? 1.f : tt - jt == 2 ? a16 : a32;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = sc[e] * (off[e] * far);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = 4 * g + e <= r ? sc[e] * on[e] : 0.f;
+          if (jt % 2 == 0)  // the tile beside it shares its k step
+#pragma unroll
+            for (int p = 0; p < PS; ++p)
+              *reinterpret_cast<u32x2*>(to + p * D::TileP + 4) = u32x2{0, 0};
+        }
+        uint32_t lo[PS], hi[PS];
+        split<PS, F32>(v[0], v[1], lo);
+        split<PS, F32>(v[2], v[3], hi);
+#pragma unroll
+        for (int p = 0; p < PS; ++p)
+          *reinterpret_cast<u32x2*>(to + p * D::TileP) = u32x2{lo[p], hi[p]};
+      }
+      // W q, and its decay
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) y[t][pt] = acc4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < NKS; ++k) {
+        bfrag qf[NT][NP];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int p = 0; p < NP; ++p)
+            qf[t][p] = frag_kperm(s_q + p * D::TileQ + (16 * t + r) * LDQ + 32 * k, g);
+        if constexpr (!F32) __builtin_amdgcn_sched_barrier(0);
+        bfrag sb[PS][PT];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) {
+          u32x4 words[PS];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            uint32_t part[PS];
+            const acc4 v = st[2 * k + e / 4][pt];
+            split<PS, F32>(v[e % 4], v[e % 4 + 1], part);
+#pragma unroll
+            for (int p = 0; p < PS; ++p) words[p][e / 2] = part[p];
+          }
+#pragma unroll
+          for (int p = 0; p < PS; ++p) sb[p][pt] = bf16x8_from_u32x4(words[p]);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int p = 0; p < NP; ++p)
+#pragma unroll
+            for (int o = 0; o + p < PS; ++o)
+#pragma unroll
+              for (int pt = 0; pt < PT; ++pt) y[t][pt] = mma_bf16(sb[o][pt], qf[t][p], y[t][pt]);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) y[t][pt] *= reach[t];
+      __syncthreads();
+    }
+    bfrag vf[NP][PT][NK];  // v, column p0 + 16 pt + r, rows 32 k + kperm
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+          vf[p][pt][k] = frag_col(s_v + p * D::TileV, LDV, 16 * (PT * wv + pt), k, g, r);
+
+    if constexpr (OUT) {
+      // + scores times v, and out: four columns of one row per lane
+      const int ldob = (int)ldo * (int)sizeof(TO);
+      const rsrc_t qo = chunk_rows(gout + t0 * ldo, ldob, rows, 16 * PT * (int)sizeof(TO));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        acc4 yp[PT];  // fp32 keeps the two sums apart: fewer roundings at the size of the output
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) yp[pt] = F32 ? acc4{0.f, 0.f, 0.f, 0.f} : y[t][pt];
+#pragma unroll
+        for (int k = 0; k <= t / 2; ++k)
+#pragma unroll
+          for (int o = 0; o < PS; ++o) {
+            const bfrag pf = *reinterpret_cast<const bfrag*>(s_p + o * D::TileP +
+                                                             (16 * t + r) * LDP + 32 * k + 8 * g);
+#pragma unroll
+            for (int p = 0; p < NP && p + o < PS; ++p)
+#pragma unroll
+              for (int pt = 0; pt < PT; ++pt) yp[pt] = mma_bf16(vf[p][pt][k], pf, yp[pt]);
+          }
+        const int row = 16 * t + r;
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) {
+          if constexpr (F32) yp[pt] += y[t][pt];
+          const int to = (back ? rows - 1 - row : row) * ldob + (16 * pt + 4 * g) * (int)sizeof(TO);
+          if constexpr (sizeof(TO) == 4) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, yp[pt]), qo, to, 0, 0);
+          } else {
+            __builtin_amdgcn_raw_buffer_store_b64(
+                __builtin_bit_cast(u32x2, bf16x4{(__bf16)yp[pt][0], (__bf16)yp[pt][1],
+                                                 (__bf16)yp[pt][2], (__bf16)yp[pt][3]}),
+                qo, to, 0, 0);
+          }
+        }
+      }
+    }
+
+    // W^T <- a^n W^T + k^T (w v)
+    if (MODE == kOutput && chunk + 1 == chunks) break;  // nobody reads this state
+    // outputs: the state before decays over the chunk; a piece's state: the chunk's part decays
+    // over the rows behind it
+    const float an = !OUT ? power(g2, len - i0 - rows) : rows < CH ? a_last : a_full;
+    const float* const weight = s_w + (rows < CH ? CH : 0);
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      u32x4 vw[NU][PT];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        acc4 wt = *reinterpret_cast<const acc4*>(weight + 32 * k + 16 * h + 4 * g);
+        if constexpr (!OUT) wt *= an;
+#pragma unroll
+        for (int e = 0; e < 4; e += 2)
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) {
+            float v[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              v[i] = (float)vf[NP - 1][pt][k][4 * h + e + i];
+#pragma unroll
+              for (int p = NP - 2; p >= 0; --p) v[i] += (float)vf[p][pt][k][4 * h + e + i];
+            }
+            uint32_t part[NU];
+            split<NU, F32>(v[0] * wt[e], v[1] * wt[e + 1], part);
+#pragma unroll
+            for (int p = 0; p < NU; ++p) vw[p][pt][2 * h + e / 2] = part[p];
+          }
+      }
+#pragma unroll
+      for (int s = 0; s < NS; s += 2) {  // two tiles: four sums between two products of one
+        if constexpr (OUT)
+          if (k == 0)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int pt = 0; pt < PT; ++pt) st[s + i][pt] *= an;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          bfrag kf[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            kf[i] = frag_col(s_k + p * D::TileK, LDK, 16 * (s + i), k, g, r);
+#pragma unroll
+          for (int o = 0; o + p < NU; ++o)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int pt = 0; pt < PT; ++pt)
+                st[s + i][pt] = mma_bf16(kf[i], bf16x8_from_u32x4(vw[o][pt]), st[s + i][pt]);
+        }
+      }
+    }
+    // every earlier row of the piece has no weight in fp32
+    if (!OUT && g2 * (double)(len - i0) < -160.) break;
+  }
+
+  if constexpr (MODE == kOutput) return;
+  float* to = nullptr;
+  if constexpr (MODE == kState)
+    to = w.pieces + ((int64_t)sg.place * a.HV + hv) * plane;
+  else if (w.last)
+    to = w.last + ((w.last_pool ? sg.slot : sg.req) * a.HV + hv) * plane;
+  if (to) {  // (walks over a transposed state leave none)
+    to += (int64_t)(p0 + r) * DK + 4 * g;
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+        *reinterpret_cast<acc4*>(to + 16 * pt * DK + 16 * s) = st[s][pt];
+  }
+}
+
+// Workgroups of a CU that the registers are held to (fp32: LDS for one at 128 and more).
+template <typename T>
+constexpr int kGroupsPerCU = sizeof(T) == 4 ? 1 : 2;
+
+// The pieces' states (OUTPUT false); the outputs of pieces, and whole requests.
+template <typename T, typename TO, int DK, int CH, int COLS, bool OUTPUT>
+__global__ __launch_bounds__(kThreads, kGroupsPerCU<T>) void linear_scan_kernel(ScanArgs a) {
+  using D = Dims<T, DK, CH, COLS>;
+  __shared__ __align__(16) char lds[OUTPUT ? D::Bytes : D::AtQ];
+  // Workgroups are dealt to the eight XCDs in turn: the walks, value heads and column blocks that
+  // read the same rows go to one of them, one after the other, and find the rows in its L2.
+  const int inner = a.walks * a.rep * a.col_blocks;
+  const int turn = blockIdx.x / 8, row = turn / inner;
+  const int unit = row * 8 + (blockIdx.x + 3 * row + row / 8) % 8;
+  int in = turn % inner;
+  const int col0 = in % a.col_blocks * COLS;
+  in /= a.col_blocks;
+  const int groups = a.HV / a.rep;
+  const Walk& w = a.walk[in / a.rep];
+  const int hv = unit % groups * a.rep + in % a.rep;
+  Segment sg;
+  if (!find_segment(a, unit / groups, sg)) return;
+  if constexpr (OUTPUT) {
+    if (sg.count > 1)
+      walk_segment<T, TO, DK, CH, COLS, kOutput>(a, w, sg, hv, col0, lds);
+    else
+      walk_segment<T, TO, DK, CH, COLS, kWhole>(a, w, sg, hv, col0, lds);
+  } else if (sg.count > 1) {
+    walk_segment<T, TO, DK, CH, COLS, kState>(a, w, sg, hv, col0, lds);
+  }
+}
+
+// Start states of a cut request's pieces, in place of the pieces' own states, and its final state.
+// A request without tokens takes its start state over into a final state of its own.
+__global__ __launch_bounds__(256) void linear_join_kernel(ScanArgs a, int plane, int parts) {
+  const Walk& w = a.walk[blockIdx.y];
+  const int part = blockIdx.x % parts;  // every parts-th run of 1024 entries from this one on
+  const int64_t pair = blockIdx.x / parts;
+  const int64_t req = pair / a.HV;
+  const int hv = (int)(pair - req * a.HV);
+  const int64_t slot = slot_of(a, req);
+  const bool live = live_slot(a, slot);
+  int len;
+  const int64_t L = end_of(a, req) - begin_of(a, req);
+  const int n = pieces_of(L, a.lseg, len);
+  const float* const home =
+      w.first ? w.first + ((w.first_pool ? slot : req) * a.HV + hv) * (int64_t)plane : nullptr;
+  float* const last =
+      w.last ? w.last + ((w.last_pool ? slot : req) * a.HV + hv) * (int64_t)plane : nullptr;
+  if (L <= 0 || !live) {
+    if (last && !w.last_pool)
+      for (int e = (part * 256 + threadIdx.x) * 4; e < plane; e += parts * 1024)
+        *reinterpret_cast<f32x4*>(last + e) =
+            live && home ? *reinterpret_cast<const f32x4*>(home + e) : f32x4{0.f, 0.f, 0.f, 0.f};
+    return;
+  }
+  if (n <= 1) return;
+  int first = 0;  // place of the request's first piece
+  for (int64_t base = 0; base < req; base += 64) {
+    const int64_t b = base + (threadIdx.x & 63);
+    int unused;
+    const int k = b < req ? pieces_of(end_of(a, b) - begin_of(a, b), a.lseg, unused) : 0;
+    first += __builtin_amdgcn_readlane(wave_inclusive(k > 1 ? k : 0), 63);
+  }
+  if (first + n > a.max_cut) return;  // cu_seqlens breaks its precondition
+  const double g2 = log2_decay(a.log_decay[hv]);
+  // the last piece of the request is shorter: the first of a walk backwards
+  const float full = power(g2, len), rest = power(g2, L - (int64_t)(n - 1) * len);
+  constexpr int AHEAD = 8;  // pieces whose states are in flight together
+  const int64_t step = (w.back ? -1 : 1) * (int64_t)a.HV * plane;
+  for (int e = (part * 256 + threadIdx.x) * 4; e < plane; e += parts * 1024) {
+    float* p = w.pieces + ((int64_t)(first + (w.back ? n - 1 : 0)) * a.HV + hv) * plane + e;
+    f32x4 s = home ? *reinterpret_cast<const f32x4*>(home + e) : f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < n; i += AHEAD, p += AHEAD * step) {
+      f32x4 mine[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        if (i + u < n) mine[u] = *reinterpret_cast<const f32x4*>(p + u * step);
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        if (i + u >= n) break;
+        *reinterpret_cast<f32x4*>(p + u * step) = s;
+        s = s * (i + u == (w.back ? 0 : n - 1) ? rest : full) + mine[u];
+      }
+    }
+    if (last) *reinterpret_cast<f32x4*>(last + e) = s;
+  }
+}
+
+// dq and dk of a group's head: the sum over its value heads, in order.
+template <typename T>
+__global__ __launch_bounds__(256) void linear_group_sum_kernel(const float* part, int64_t step,
+                                                               T* out0, T* out1,
+                                                               const int64_t* idx,
+                                                               const int64_t* cu, int64_t B,
+                                                               int64_t N, int64_t npool, int H,
+                                                               int rep, int d) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= N * H * d) return;
+  const int64_t t = i / ((int64_t)H * d);
+  if (t < cu[0] || t >= cu[B]) return;
+  if (idx) {
+    const int64_t slot = idx[request_of(cu, B, t)];
+    if (slot < 0 || slot >= npool) return;
+  }
+  const int64_t th = i / d;
+  const float* p = part + blockIdx.y * step + th * rep * d + (i - th * d);
+  f32x4 s = *reinterpret_cast<const f32x4*>(p);
+  for (int r = 1; r < rep; ++r) s += *reinterpret_cast<const f32x4*>(p + r * d);
+  const float v[4] = {s[0], s[1], s[2], s[3]};
+  store_vec<4>((blockIdx.y ? out1 : out0) + i, v);
+}
+
+// Tokens of a piece at most, 0: no request is cut. A workgroup's time goes with its tokens, and
+// `slots` of them run at a time, so pieces are sized to fill k rounds of the device, with half a
+// piece more for every request, k = 1 .. 4: more rounds even out pieces of different lengths, fewer
+// spare the joins, which cost what kPieceTokens tokens do.
+constexpr int kPieceTokens = 1000;
+constexpr int64_t kSlots = 512;
+
+int cols_of(int rows) { return rows == 64 ? 64 : 128; }
+
+int cut_of(const LinearShape& s, int rows, int walks) {
+  const int64_t blocks = (int64_t)s.HV * (rows / cols_of(rows)) * walks;
+  int64_t best = 0, cost = INT64_MAX;
+  for (int k = 1; k <= 4; ++k) {
+    const int64_t pieces2 = 2 * k * kSlots / blocks - s.B;  // twice the pieces for N tokens
+    if (pieces2 <= 0) continue;
+    const int64_t l = cdiv(cdiv(2 * s.N, pieces2), 64) * 64;
+    if (k * (l + kPieceTokens) < cost) {
+      cost = k * (l + kPieceTokens);
+      best = l;
+    }
+  }
+  if (best < 512) best = best == 0 ? 0 : 512;
+  return best == 0 || s.N <= best ? 0 : (int)best;
+}
+
+int forward_cut(const LinearShape& s) { return cut_of(s, s.dv, 1); }
+int backward_cut(const LinearShape& s) { return cut_of(s, s.dv > s.dk ? s.dv : s.dk, 3); }
+
+// Requests of at most this many tokens run token by token, where the mean length says that most
+// are and there are enough to fill the device (a call that splits pays a launch for the longer
+// ones too).
+int short_tokens(const LinearShape& s) {
+  return s.N <= 4 * s.B && s.B * s.HV * (s.dv / 64) >= 2048 ? 4 : 0;
+}
+
+// Pieces of cut requests: one of L tokens has at most L / lseg + 1, and each request that is cut has
+// more than lseg tokens, so that there are at most min(B, N / lseg) of them.
+int64_t max_cut(const LinearShape& s, int lseg) {
+  if (!lseg) return 0;
+  const int64_t full = s.N / lseg;
+  return full + (s.B < full ? s.B : full);
+}
+
+size_t piece_bytes(const LinearShape& s, int lseg) {
+  return align256((size_t)max_cut(s, lseg) * s.HV * s.dv * s.dk * sizeof(float));
+}
+
+int64_t scan_blocks(const ScanArgs& a) {
+  const int64_t segments = a.nreq + (a.lseg ? a.N / a.lseg : 0);
+  return cdiv(segments * (a.HV / a.rep), 8) * 8 * a.walks * a.rep * a.col_blocks;
+}
+
+// Workgroups of a state in the join: enough to fill the device, few where many requests are likely
+// not cut.
+int join_parts(const LinearShape& s) {
+  int parts = s.dv * s.dk / 1024;
+  while (parts > 1 && s.B * s.HV * (parts / 2) >= 2048) parts /= 2;
+  return parts;
+}
+
+template <typename T, typename TO, int DK, int COLS, bool OUTPUT>
+hipError_t launch_cols(const ScanArgs& a, hipStream_t st) {
+  constexpr int CH = sizeof(T) == 4 || DK == 256 ? 32 : 64;
+  hipLaunchKernelGGL((linear_scan_kernel<T, TO, DK, CH, COLS, OUTPUT>),
+                     dim3((unsigned)scan_blocks(a)), dim3(kThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+// W is rows x dk.
+template <typename T, typename TO, bool OUTPUT>
+hipError_t launch_scan(ScanArgs& a, int rows, int dk, hipStream_t st) {
+  a.rows = rows;
+  a.col_blocks = rows / cols_of(rows);
+#define GDN_LINEAR_CASE(DK)                                                  \
+  if (dk == DK)                                                              \
+    return rows == 64 ? launch_cols<T, TO, DK, 64, OUTPUT>(a, st)            \
+                      : launch_cols<T, TO, DK, 128, OUTPUT>(a, st);
+  GDN_LINEAR_CASE(64)
+  GDN_LINEAR_CASE(128)
+  GDN_LINEAR_CASE(256)
+#undef GDN_LINEAR_CASE
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_join(const LinearShape& s, const ScanArgs& a, hipStream_t st) {
+  const int parts = join_parts(s);
+  hipLaunchKernelGGL(linear_join_kernel, dim3((unsigned)(s.B * s.HV * parts), (unsigned)a.walks),
+                     dim3(256), 0, st, a, s.dv * s.dk, parts);
+  return hipGetLastError();
+}
+
+ScanArgs scan_args(const LinearShape& s, const float* log_decay, const int64_t* idx,
+                   const int64_t* cu, int lseg) {
+  ScanArgs a{};
+  a.log_decay = log_decay;
+  a.idx = idx;
+  a.cu = cu;
+  a.N = s.N;
+  a.nreq = s.B;
+  a.npool = s.pool;
+  a.HV = s.HV;
+  a.rep = s.HV / s.H;
+  a.lseg = lseg;
+  a.max_cut = (int)max_cut(s, lseg);
+  return a;
+}
+
+#define GDN_TRY(call)                                  \
+  if (const hipError_t e_ = (call); e_ != hipSuccess) return e_
+
+template <typename T>
+hipError_t forward(const LinearShape& s, const void* q, const void* k, const void* v,
+                   const float* log_decay, float* state, const int64_t* idx, const int64_t* cu,
+                   void* out, char* ws, hipStream_t st) {
+  ScanArgs a = scan_args(s, log_decay, state ? idx : nullptr, cu, forward_cut(s));
+  const int rep = a.rep;
+  a.short_len = short_tokens(s);
+  if (a.short_len)
+    GDN_TRY(launch_linear_short(s, q, k, v, log_decay, state, idx, cu, out, a.short_len, st));
+  a.walks = 1;
+  a.walk[0] = Walk{q,   k,     v,     s.ldq,      s.ldk, s.ldv, rep, rep, 1,
+                   out, state, state, (float*)ws, 1,     1,     0,   0,   s.scale, 1.f};
+  if (a.lseg) {
+    GDN_TRY((launch_scan<T, T, false>(a, s.dv, s.dk, st)));
+    GDN_TRY(launch_join(s, a, st));
+  }
+  return launch_scan<T, T, true>(a, s.dv, s.dk, st);
+}
+
+template <typename T, typename TP>  // TP: dq and dk, fp32 partial sums where heads are shared
+hipError_t backward(const LinearShape& s, const void* q, const void* k, const void* v,
+                    const float* log_decay, const float* state, const int64_t* idx,
+                    const int64_t* cu, const void* dout, const float* dstate, void* dq, void* dk,
+                    void* dv, float* dstate0, char* ws, hipStream_t st) {
+  const int lseg = backward_cut(s);
+  ScanArgs a = scan_args(s, log_decay, state ? idx : nullptr, cu, lseg);
+  const int rep = a.rep;
+  const int64_t ldo = (int64_t)s.HV * s.dv;
+  float* const ps = (float*)ws;
+  float* const pd = (float*)(ws + piece_bytes(s, lseg));
+  float* const part = (float*)(ws + 2 * piece_bytes(s, lseg));
+  const int64_t step = s.N * s.HV * s.dk;
+  const Walk wq{dout, v,     k,       ldo, s.ldv, s.ldk, 1, 1, rep, rep > 1 ? (void*)part : dq,
+                state, nullptr, ps,    1,   0,     1,     0, s.scale, 1.f};
+  const Walk wk{v,      dout,    q,  s.ldv, ldo, s.ldq, 1, 1, rep, rep > 1 ? (void*)(part + step) : dk,
+                dstate, nullptr, pd, 0,     0,   1,     1, 1.f, s.scale};
+  const Walk wv{k,      q,       dout, s.ldk, s.ldq, ldo, rep, rep, 1, dv,
+                dstate, dstate0, pd,   0,     0,     0,   1,   1.f, s.scale};
+  if (lseg) {
+    a.walks = 2;
+    a.walk[0] = Walk{q,     k,       v,  s.ldq, s.ldk, s.ldv, rep, rep, 1, nullptr,
+                     state, nullptr, ps, 1,     0,     0,     0,   1.f, 1.f};
+    a.walk[1] = wv;
+    GDN_TRY((launch_scan<T, T, false>(a, s.dv, s.dk, st)));
+  } else {
+    a.walks = 1;
+    a.walk[0] = wv;
+  }
+  if (lseg || dstate0) GDN_TRY(launch_join(s, a, st));
+  if (s.N == 0) return hipSuccess;
+  if (s.dk == s.dv && rep == 1) {
+    a.walks = 3;
+    a.walk[0] = wv;
+    a.walk[1] = wk;
+    a.walk[2] = wq;
+    return launch_scan<T, T, true>(a, s.dv, s.dk, st);
+  }
+  a.walks = 1;
+  a.walk[0] = wv;
+  GDN_TRY((launch_scan<T, T, true>(a, s.dv, s.dk, st)));
+  a.walks = 2;
+  a.walk[0] = wk;
+  a.walk[1] = wq;
+  GDN_TRY((launch_scan<T, TP, true>(a, s.dk, s.dv, st)));
+  if (rep == 1) return hipSuccess;
+  hipLaunchKernelGGL(linear_group_sum_kernel<T>, dim3((unsigned)cdiv(s.N * s.H * s.dk, 1024), 2),
+                     dim3(256), 0, st, part, step, (T*)dq, (T*)dk, a.idx, cu, s.B, s.N, s.pool, s.H,
+                     rep, s.dk);
+  return hipGetLastError();
+}
+
+bool scan_grids_fit(const LinearShape& s, int lseg, int rows, int walks) {
+  ScanArgs a = scan_args(s, nullptr, nullptr, nullptr, lseg);
+  a.walks = walks;
+  a.col_blocks = rows / cols_of(rows);
+  return grid_ok(scan_blocks(a), kThreads) && grid_ok(s.B * s.HV * join_parts(s), 256);
+}
+
+}  // namespace
+
+size_t linear_workspace(const LinearShape& s) { return piece_bytes(s, forward_cut(s)); }
+
+size_t linear_bwd_workspace(const LinearShape& s) {
+  return 2 * piece_bytes(s, backward_cut(s)) +
+         (s.HV > s.H ? align256(2 * sizeof(float) * s.N * s.HV * s.dk) : 0);
+}
+
+bool linear_prefill_grids_fit(const LinearShape& s) {
+  return scan_grids_fit(s, forward_cut(s), s.dv, 1) &&
+         (!short_tokens(s) || linear_token_grid_fits(s));
+}
+
+bool linear_bwd_grids_fit(const LinearShape& s) {
+  const int lseg = backward_cut(s);
+  return scan_grids_fit(s, lseg, s.dv, 3) && scan_grids_fit(s, lseg, s.dk, 3) &&
+         grid_ok(cdiv(s.N * s.H * s.dk, 1024), 256);
+}
+
+hipError_t launch_linear_prefill(const LinearShape& s, const void* q, const void* k, const void* v,
+                                 const float* log_decay, float* state, const int64_t* idx,
+                                 const int64_t* cu, void* out, char* ws, hipStream_t st) {
+  return s.bf16 ? forward<__bf16>(s, q, k, v, log_decay, state, idx, cu, out, ws, st)
+                : forward<float>(s, q, k, v, log_decay, state, idx, cu, out, ws, st);
+}
+
+hipError_t launch_linear_bwd(const LinearShape& s, const void* q, const void* k, const void* v,
+                             const float* log_decay, const float* state, const int64_t* idx,
+                             const int64_t* cu, const void* dout, const float* dstate, void* dq,
+                             void* dk, void* dv, float* dstate0, char* ws, hipStream_t st) {
+  if (!s.bf16)
+    return backward<float, float>(s, q, k, v, log_decay, state, idx, cu, dout, dstate, dq, dk, dv,
+                                  dstate0, ws, st);
+  return s.HV > s.H ? backward<__bf16, float>(s, q, k, v, log_decay, state, idx, cu, dout, dstate,
+                                              dq, dk, dv, dstate0, ws, st)
+                    : backward<__bf16, __bf16>(s, q, k, v, log_decay, state, idx, cu, dout, dstate,
+                                               dq, dk, dv, dstate0, ws, st);
+}
+
+}  // namespace layer
+}  // namespace gdn

@@ -499,7 +499,9 @@ typedef struct {
  * shape alone.
  * A non-finite v also reaches that column of the up to 31 tokens before it in its request, and
  * need not reach the states behind its piece once its decay there is zero in fp32. Every finite
- * value is taken as it is; an infinite one may stand as NaN in whatever it reaches.
+ * value is taken as it is, but products of an entry of q with one of k have to stay inside fp32's
+ * range: below 2^-126 they count as zero, above it they are infinite. An infinite value may stand as
+ * NaN in whatever it reaches.
  * q, k, v, out and state_pool 16-byte aligned. workspace: at least gdn_linear_workspace_size
  * bytes, 256-byte aligned; its contents on entry do not matter. N == 0 or B == 0 is a no-op. */
 size_t gdn_linear_workspace_size(const gdn_linear_problem_t* prob);

@@ -220,12 +220,33 @@ def test_linear_non_finite_values_stay_in_their_request():
 
 
 def test_linear_large_values():
-    """Finite values up to the largest of bf16 next to small ones."""
+    """Finite values up to the largest of bf16 next to small ones. Here an entry of q times one of k
+    is about 1e-38: fp32 ends at 2^-126 = 1.2e-38, and a score whose 64 products each lose up to that
+    is 64 2^-126 off, which v, the decays and the scale carry into the output."""
     c = make(14, [80], 1, 1, 64, 64, "bf16", log_decay=[-0.1])
     for name, scale in (("q", 1e-20), ("k", 1e-18), ("v", 1e37)):
         c[name], c[name + "64"] = rounded(scale * c[name + "64"], "bf16")
     c["pool"], c["pool64"] = f32(1e18 * c["pool64"])
-    check_forward(c, *forward(c), "linear large values")
+    out, state = forward(c)
+    ref, new, mag, mags, _ = L.linear_fwd(*args64(c))
+    lost = np.zeros_like(ref)
+    carried = 0.0
+    for t in range(80):
+        carried = np.exp(-0.1) * carried + np.abs(c["v64"][t])
+        lost[t] = c["scale"] * 64 * 2.0 ** -126 * carried
+    h = HALF["bf16"]
+    within(out, ref, h * np.abs(ref) + (1 + h) * (OUT["bf16"] * mag + lost), "linear large values")
+    within(state, new, STATE * mags, "linear large values, state")
+
+
+def test_linear_wide_range_of_values():
+    """Values of very different sizes whose products stay inside fp32's range."""
+    for q, k, v, pool in ((1e-12, 1e-18, 1e37, 1e18), (1e15, 1e15, 1e-30, 1e-14), (1e-15, 1e25, 1e10, 1e34)):
+        c = make(14, [80], 1, 1, 64, 64, "bf16", log_decay=[-0.1])
+        for name, scale in (("q", q), ("k", k), ("v", v)):
+            c[name], c[name + "64"] = rounded(scale * c[name + "64"], "bf16")
+        c["pool"], c["pool64"] = f32(pool * c["pool64"])
+        check_forward(c, *forward(c), f"linear values of {q}, {k}, {v}")
 
 
 def test_linear_calls_repeat_to_the_bit():
