@@ -40,6 +40,30 @@ namespace {
 using mfma::kperm;
 using mfma::mma_bf16;
 
+// -1 beside either half of a register of two bf16. (Kept in registers: as literals they are taken
+// for something else.)
+struct Minus {
+  uint32_t lo = 0x0000BF80u, hi = 0xBF800000u;
+  __device__ __forceinline__ Minus() { asm("" : "+v"(lo), "+v"(hi)); }
+};
+// a and b as sums of P bf16 each as split() forms them: what is left behind a part cut off comes from
+// one two-term product each, where taking the parts out as fp32 and subtracting them takes two.
+template <int P, bool PAIRS>
+__device__ __forceinline__ void split_by(const Minus& m, float a, float b, uint32_t (&part)[P]) {
+  if constexpr (PAIRS) {
+    split<P, true>(a, b, part);
+  } else {
+#pragma unroll
+    for (int p = 0; p + 1 < P; ++p) {
+      part[p] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
+      const bf16x2 top = __builtin_bit_cast(bf16x2, part[p]);
+      a = __builtin_amdgcn_fdot2_f32_bf16(top, __builtin_bit_cast(bf16x2, m.lo), a, false);
+      b = __builtin_amdgcn_fdot2_f32_bf16(top, __builtin_bit_cast(bf16x2, m.hi), b, false);
+    }
+    part[P - 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+  }
+}
+
 struct Walk {
   const void *q, *k, *v;
   int64_t ldq, ldk, ldv;  // elements between tokens
@@ -47,14 +71,14 @@ struct Walk {
   void* out;              // [N, HV, rows] dense; in the states' pass the pieces' states
   const float* first;     // states in front of the walk, NULL: zero
   float* last;            // ... behind it, NULL: not wanted
-  float* pieces;          // states of the pieces of cut requests: [places][HV][rows][DK]
+  float* pieces;          // of cut requests: [places][HV][rows][DK], the pieces' states, then their
+                          // start states
   int first_pool, last_pool;  // by slot of the pool, else by request
   int transposed;         // states lie in memory as [DK][rows]
   int back;               // from the last token to the first
   float read, write;
 };
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kWalks = 3;
 struct ScanArgs {
   Walk walk[kWalks];
@@ -88,7 +112,9 @@ struct Segment {
   int place;       // among the pieces of cut requests (cut requests only)
 };
 
-// Segment number `seg` of the call, by a scan over the requests, 64 at a time in every wave.
+// Segment number `seg` of the call (ALL false: of its cut requests), by a scan over the requests, 64
+// at a time in every wave.
+template <bool ALL>
 __device__ __forceinline__ bool find_segment(const ScanArgs& a, int seg, Segment& s) {
   const int lane = threadIdx.x & 63;
   int len = 0, index = 0;
@@ -103,8 +129,10 @@ __device__ __forceinline__ bool find_segment(const ScanArgs& a, int seg, Segment
     for (int64_t base = 0; base < a.nreq; base += 64) {
       const int64_t b = base + lane;
       int mine = 0;
-      const int n = b < a.nreq ? pieces_of(end_of(a, b) - begin_of(a, b), a.lseg, mine) : 0;
-      const int inc = wave_inclusive(n), cut = wave_inclusive(n > 1 ? n : 0);
+      int n = b < a.nreq ? pieces_of(end_of(a, b) - begin_of(a, b), a.lseg, mine) : 0;
+      const int cut = wave_inclusive(n > 1 ? n : 0);
+      if (!ALL && n == 1) n = 0;
+      const int inc = ALL ? wave_inclusive(n) : cut;
       const uint64_t over = __ballot(before + inc > seg);
       if (over) {
         const int k = __builtin_ctzll(over);
@@ -142,33 +170,45 @@ __device__ __forceinline__ float power(double g2, int64_t n) {
   return __builtin_amdgcn_ldexpf(exp2_((float)(p - whole)), (int)whole);
 }
 
+// Whether a state may still be seen n rows later (fp32 ends at 2^-149).
+__device__ __forceinline__ bool reaches(double g2, int64_t n) { return !(g2 * (double)n < -160.); }
+
 // Staging of a tile of CH rows x COLS entries: 16-byte pieces in registers between the load and
 // the LDS store, so that the next chunk's rows travel while this one is worked on. Walks backwards
 // take the rows in reverse order.
-template <typename T, int CH, int COLS>
+template <typename T, int CH, int COLS, int THREADS>
 struct Stage {
   static constexpr int V = 16 / (int)sizeof(T);
-  static constexpr int PER_ROW = COLS / V, PIECES = CH * PER_ROW / kThreads;
-  static constexpr int ROWS = kThreads / PER_ROW;  // rows of one piece of all threads
-  static_assert(CH * PER_ROW % kThreads == 0 && kThreads % PER_ROW == 0, "whole rows at a time");
+  static constexpr int PER_ROW = COLS / V, PIECES = CH * PER_ROW / THREADS;
+  static constexpr int ROWS = THREADS / PER_ROW;  // rows of one piece of all threads
+  static_assert(CH * PER_ROW % THREADS == 0 && THREADS % PER_ROW == 0, "whole rows at a time");
   u32x4 r[PIECES];
-  __device__ __forceinline__ void load(const T* base, int64_t ld, int rows, bool back) {
-    const int ldb = (int)ld * (int)sizeof(T), row = (int)threadIdx.x / PER_ROW;
-    const rsrc_t q = chunk_rows(base, ldb, rows, COLS * (int)sizeof(T));
-    // (a row in front of the tile has an offset below zero, beyond every size as an unsigned one)
-    const int at = (back ? rows - 1 - row : row) * ldb + (int)(threadIdx.x % PER_ROW) * 16;
-    const int step = back ? -ROWS * ldb : ROWS * ldb;
+  const T* base;
+  int ld;
+  int at, dir;  // a lane's byte offset in a full tile, bytes from row to row of the walk
+  __device__ __forceinline__ void init(const void* from, int64_t first, int64_t stride, bool back) {
+    base = reinterpret_cast<const T*>(from) + first;
+    ld = (int)stride;
+    dir = (back ? -1 : 1) * (int)stride * (int)sizeof(T);
+    at = (int)threadIdx.x / PER_ROW * dir + (int)(threadIdx.x % PER_ROW) * 16;
+  }
+  // t: the lowest token of the chunk. (A row in front of it has an offset below zero, beyond every
+  // size as an unsigned one.)
+  __device__ __forceinline__ void load(int64_t t, int rows) {
+    const int ldb = ld * (int)sizeof(T);
+    const rsrc_t q = chunk_rows(base + t * ld, ldb, rows, COLS * (int)sizeof(T));
+    const int from = at + (dir < 0 ? (rows - 1) * ldb : 0);
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
-      r[i] = __builtin_bit_cast(u32x4,
-                                __builtin_amdgcn_raw_buffer_load_b128(q, at + i * step, 0, 0));
+      r[i] = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(q, from + i * ROWS * dir, 0, 0));
   }
   // as NP tiles of bf16 parts, `plane` entries apart
   template <int NP, bool WIDE>
   __device__ __forceinline__ void store(__bf16* to, int plane, int ld) const {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      const int p = i * kThreads + threadIdx.x, row = p / PER_ROW, c = p % PER_ROW * V;
+      const int p = i * THREADS + threadIdx.x, row = p / PER_ROW, c = p % PER_ROW * V;
       if constexpr (NP == 1) {
         if constexpr (WIDE) {
           *reinterpret_cast<u32x4*>(to + row * ld + c) = r[i];
@@ -211,9 +251,13 @@ __device__ __forceinline__ bool deal(int wave, int i, int& tt, int& jt) {
 // piece from zero; the outputs of a piece from its start state.
 enum Mode { kWhole, kState, kOutput };
 
+// Outputs: four waves. States: a wave for every 16 of W's rows, so that there are enough to fill the
+// waits between a chunk's steps.
+template <int COLS, bool OUTPUT>
+constexpr int kThreads = OUTPUT ? 256 : 4 * COLS;
+
 template <typename T, int DK, int CH, int COLS>
 struct Dims {
-  static constexpr int PT = COLS / 64;  // tiles of 16 of W's rows a wave
   static constexpr int NP = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of an input
   static constexpr int PS = sizeof(T) == 4 ? 3 : 2;  // ... of the decayed scores and of W in W q
   // LDS rows. q is read in 8-byte pieces down 16 rows: fewest conflicts where the stride is 2 mod
@@ -230,8 +274,10 @@ template <typename T, typename TO, int DK, int CH, int COLS, Mode MODE>
 __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, const Segment& sg,
                                              int hv, int col0, char* lds) {
   using D = Dims<T, DK, CH, COLS>;
+  constexpr int THREADS = kThreads<COLS, MODE != kState>;
+  constexpr int PT = COLS * 4 / THREADS;  // tiles of 16 of W's rows a wave
   constexpr bool F32 = sizeof(T) == 4, OUT = MODE != kState;
-  constexpr int NP = D::NP, PS = D::PS, PT = D::PT;
+  constexpr int NP = D::NP, PS = D::PS;
   // ... of the update's decayed v: the state of a piece's outputs is only read by W q
   constexpr int NU = MODE == kOutput ? PS : 3;
   constexpr int NT = CH / 16, NK = CH / 32;    // token tiles, k steps over tokens
@@ -251,11 +297,11 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
   const bool back = w.back != 0;
   const int rows_all = a.rows;
 
-  const T* const gq = reinterpret_cast<const T*>(w.q) + (int64_t)(hv / w.rq) * DK;
-  const T* const gk = reinterpret_cast<const T*>(w.k) + (int64_t)(hv / w.rk) * DK;
-  const T* const gv = reinterpret_cast<const T*>(w.v) + (int64_t)(hv / w.rv) * rows_all + col0;
   TO* const gout = reinterpret_cast<TO*>(w.out) + (int64_t)hv * rows_all + p0;
-  const int64_t ldo = (int64_t)a.HV * rows_all, plane = (int64_t)rows_all * DK;
+  const int64_t ldo = (int64_t)a.HV * rows_all;
+  const int ldob = (int)ldo * (int)sizeof(TO);
+  const int out_dir = back ? -ldob : ldob;
+  const int64_t plane = (int64_t)rows_all * DK;
 
   // W^T: st[s tile][column tile], entries 16 s + 4 g .. + 3 of column p0 + 16 pt + r
   acc4 st[NS][PT];
@@ -287,25 +333,29 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
         st[s][pt] = *reinterpret_cast<const acc4*>(from + 16 * pt * DK + 16 * s);
   }
 
-  Stage<T, CH, DK> qk, qq;  // the next chunk's rows
-  Stage<T, CH, COLS> qv;
+  Stage<T, CH, DK, THREADS> qk, qq;  // the next chunk's rows
+  Stage<T, CH, COLS, THREADS> qv;
   const int len = (int)(sg.t1 - sg.t0), chunks = (len + CH - 1) / CH;
   // Chunks in the order of the walk; a piece's state alone is summed from the walk's end.
   auto place = [&](int n) { return (OUT ? n : chunks - 1 - n) * CH; };
   auto rows_at = [&](int i0) { return len - i0 < CH ? len - i0 : CH; };
   auto token_at = [&](int i0) {  // the lowest of the chunk
-    return back ? sg.t1 - i0 - rows_at(i0) : sg.t0 + i0;
+    return sg.t0 + (back ? len - i0 - rows_at(i0) : i0);
   };
+  qk.init(w.k, (int64_t)(hv / w.rk) * DK, w.ldk, back);
+  if constexpr (OUT) qq.init(w.q, (int64_t)(hv / w.rq) * DK, w.ldq, back);
+  qv.init(w.v, (int64_t)(hv / w.rv) * rows_all + col0, w.ldv, back);
   auto fetch = [&](int i0) {
     const int rows = rows_at(i0);
     const int64_t t = token_at(i0);
-    qk.load(gk + t * w.ldk, w.ldk, rows, back);
-    if constexpr (OUT) qq.load(gq + t * w.ldq, w.ldq, rows, back);
-    qv.load(gv + t * w.ldv, w.ldv, rows, back);
+    qk.load(t, rows);
+    if constexpr (OUT) qq.load(t, rows);
+    qv.load(t, rows);
   };
   fetch(place(0));
 
   // Decays. Scores: row r of a tile against its columns 4 g + e, on the diagonal and one tile off.
+  const Minus minus;
   const double g2 = log2_decay(a.log_decay[hv]);
   const int nlast = len - (chunks - 1) * CH;
   float on[4], off[4], reach[NT];
@@ -326,8 +376,18 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
     s_w[CH + tid] = tid < nlast ? w.write * power(g2, nlast - 1 - tid + w.back) : 0.f;
   }
   const float a_full = power(g2, CH), a_last = power(g2, nlast);
+  // The first chunk's rows are waited for here: what is on its way when the loop is entered would
+  // make every turn wait for the stores of the one before it.
+  __builtin_amdgcn_s_waitcnt(0x0F70);
 
   for (int chunk = 0; chunk < chunks; ++chunk) {
+    if constexpr (OUT) {
+      // Places in LDS are formed anew for every chunk: kept in registers they spill, and a reload
+      // waits for the next chunk's rows, which were asked for before it.
+      asm volatile("" : "+v"(lane));
+      r = lane & 15;
+      g = lane >> 4;
+    }
     const int i0 = place(chunk), rows = rows_at(i0);
     const int64_t t0 = token_at(i0);
     if (chunk > 0) __syncthreads();  // the chunk before has been read
@@ -337,6 +397,9 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
     __syncthreads();
     if (chunk + 1 < chunks) fetch(place(chunk + 1));
 
+    // outputs: the state before decays over the chunk; a piece's state: the chunk's part decays
+    // over the rows behind it
+    const float an = !OUT ? power(g2, len - i0 - rows) : rows < CH ? a_last : a_full;
     acc4 y[NT][PT];  // out^T: columns 16 pt + 4 g .. + 3 of row 16 t + r
     if constexpr (OUT) {
       // scores^T, j x i: each wave some of the tiles, decayed
@@ -375,8 +438,8 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
               *reinterpret_cast<u32x2*>(to + p * D::TileP + 4) = u32x2{0, 0};
         }
         uint32_t lo[PS], hi[PS];
-        split<PS, F32>(v[0], v[1], lo);
-        split<PS, F32>(v[2], v[3], hi);
+        split_by<PS, F32>(minus, v[0], v[1], lo);
+        split_by<PS, F32>(minus, v[2], v[3], hi);
 #pragma unroll
         for (int p = 0; p < PS; ++p)
           *reinterpret_cast<u32x2*>(to + p * D::TileP) = u32x2{lo[p], hi[p]};
@@ -402,8 +465,11 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             uint32_t part[PS];
-            const acc4 v = st[2 * k + e / 4][pt];
-            split<PS, F32>(v[e % 4], v[e % 4 + 1], part);
+            acc4& w4 = st[2 * k + e / 4][pt];
+            const float v0 = w4[e % 4], v1 = w4[e % 4 + 1];
+            w4[e % 4] = v0 * an;  // the decay over the chunk
+            w4[e % 4 + 1] = v1 * an;
+            split_by<PS, F32>(minus, v0, v1, part);
 #pragma unroll
             for (int p = 0; p < PS; ++p) words[p][e / 2] = part[p];
           }
@@ -436,7 +502,7 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
 
     if constexpr (OUT) {
       // + scores times v, and out: four columns of one row per lane
-      const int ldob = (int)ldo * (int)sizeof(TO);
+      const int out0 = back ? (rows - 1) * ldob : 0;
       const rsrc_t qo = chunk_rows(gout + t0 * ldo, ldob, rows, 16 * PT * (int)sizeof(TO));
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -458,7 +524,7 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt) {
           if constexpr (F32) yp[pt] += y[t][pt];
-          const int to = (back ? rows - 1 - row : row) * ldob + (16 * pt + 4 * g) * (int)sizeof(TO);
+          const int to = out0 + row * out_dir + (16 * pt + 4 * g) * (int)sizeof(TO);
           if constexpr (sizeof(TO) == 4) {
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, yp[pt]), qo, to, 0, 0);
           } else {
@@ -471,11 +537,8 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
       }
     }
 
-    // W^T <- a^n W^T + k^T (w v)
+    // W^T (decayed by now) += k^T (w v)
     if (MODE == kOutput && chunk + 1 == chunks) break;  // nobody reads this state
-    // outputs: the state before decays over the chunk; a piece's state: the chunk's part decays
-    // over the rows behind it
-    const float an = !OUT ? power(g2, len - i0 - rows) : rows < CH ? a_last : a_full;
     const float* const weight = s_w + (rows < CH ? CH : 0);
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
@@ -496,19 +559,24 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
               for (int p = NP - 2; p >= 0; --p) v[i] += (float)vf[p][pt][k][4 * h + e + i];
             }
             uint32_t part[NU];
-            split<NU, F32>(v[0] * wt[e], v[1] * wt[e + 1], part);
+            split_by<NU, F32>(minus, v[0] * wt[e], v[1] * wt[e + 1], part);
 #pragma unroll
             for (int p = 0; p < NU; ++p) vw[p][pt][2 * h + e / 2] = part[p];
           }
       }
 #pragma unroll
       for (int s = 0; s < NS; s += 2) {  // two tiles: four sums between two products of one
-        if constexpr (OUT)
-          if (k == 0)
+        // Where the state is a result, 32 rows are summed on their own and join it in one
+        // addition: the matrix instructions cut off what does not fit beside a large sum
+        // (131072 tokens: states 1.6e-7 off instead of 5.8e-7; at DK = 256 whole requests have no
+        // registers for it).
+        constexpr bool APART = MODE == kState || F32 || (MODE == kWhole && DK < 256);
+        acc4 sum[2][PT];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int pt = 0; pt < PT; ++pt) st[s + i][pt] *= an;
+          for (int pt = 0; pt < PT; ++pt)
+            sum[i][pt] = APART ? acc4{0.f, 0.f, 0.f, 0.f} : st[s + i][pt];
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           bfrag kf[2];
@@ -521,12 +589,17 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
             for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int pt = 0; pt < PT; ++pt)
-                st[s + i][pt] = mma_bf16(kf[i], bf16x8_from_u32x4(vw[o][pt]), st[s + i][pt]);
+                sum[i][pt] = mma_bf16(kf[i], bf16x8_from_u32x4(vw[o][pt]), sum[i][pt]);
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt)
+            st[s + i][pt] = APART ? st[s + i][pt] + sum[i][pt] : sum[i][pt];
       }
     }
     // every earlier row of the piece has no weight in fp32
-    if (!OUT && g2 * (double)(len - i0) < -160.) break;
+    if (!OUT && !reaches(g2, len - i0)) break;
   }
 
   if constexpr (MODE == kOutput) return;
@@ -546,12 +619,13 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
 }
 
 // Workgroups of a CU that the registers are held to (fp32: LDS for one at 128 and more).
-template <typename T>
+template <typename T, int DK, bool OUTPUT>
 constexpr int kGroupsPerCU = sizeof(T) == 4 ? 1 : 2;
 
 // The pieces' states (OUTPUT false); the outputs of pieces, and whole requests.
 template <typename T, typename TO, int DK, int CH, int COLS, bool OUTPUT>
-__global__ __launch_bounds__(kThreads, kGroupsPerCU<T>) void linear_scan_kernel(ScanArgs a) {
+__global__ __launch_bounds__((kThreads<COLS, OUTPUT>),
+                             (kGroupsPerCU<T, DK, OUTPUT> * kThreads<COLS, OUTPUT> / 256)) void linear_scan_kernel(ScanArgs a) {
   using D = Dims<T, DK, CH, COLS>;
   __shared__ __align__(16) char lds[OUTPUT ? D::Bytes : D::AtQ];
   // Workgroups are dealt to the eight XCDs in turn: the walks, value heads and column blocks that
@@ -566,23 +640,21 @@ __global__ __launch_bounds__(kThreads, kGroupsPerCU<T>) void linear_scan_kernel(
   const Walk& w = a.walk[in / a.rep];
   const int hv = unit % groups * a.rep + in % a.rep;
   Segment sg;
-  if (!find_segment(a, unit / groups, sg)) return;
-  if constexpr (OUTPUT) {
-    if (sg.count > 1)
-      walk_segment<T, TO, DK, CH, COLS, kOutput>(a, w, sg, hv, col0, lds);
-    else
-      walk_segment<T, TO, DK, CH, COLS, kWhole>(a, w, sg, hv, col0, lds);
-  } else if (sg.count > 1) {
+  if (!find_segment<OUTPUT>(a, unit / groups, sg)) return;
+  if constexpr (!OUTPUT)
     walk_segment<T, TO, DK, CH, COLS, kState>(a, w, sg, hv, col0, lds);
-  }
+  else if (sg.count > 1)
+    walk_segment<T, TO, DK, CH, COLS, kOutput>(a, w, sg, hv, col0, lds);
+  else
+    walk_segment<T, TO, DK, CH, COLS, kWhole>(a, w, sg, hv, col0, lds);
 }
 
 // Start states of a cut request's pieces, in place of the pieces' own states, and its final state.
 // A request without tokens takes its start state over into a final state of its own.
-__global__ __launch_bounds__(256) void linear_join_kernel(ScanArgs a, int plane, int parts) {
+__global__ __launch_bounds__(256) void linear_join_kernel(ScanArgs a, int plane, int blocks) {
   const Walk& w = a.walk[blockIdx.y];
-  const int part = blockIdx.x % parts;  // every parts-th run of 1024 entries from this one on
-  const int64_t pair = blockIdx.x / parts;
+  const int part = blockIdx.x % blocks;  // every blocks-th run of 1024 entries from this one on
+  const int64_t pair = blockIdx.x / blocks;
   const int64_t req = pair / a.HV;
   const int hv = (int)(pair - req * a.HV);
   const int64_t slot = slot_of(a, req);
@@ -596,7 +668,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(ScanArgs a, int plane,
       w.last ? w.last + ((w.last_pool ? slot : req) * a.HV + hv) * (int64_t)plane : nullptr;
   if (L <= 0 || !live) {
     if (last && !w.last_pool)
-      for (int e = (part * 256 + threadIdx.x) * 4; e < plane; e += parts * 1024)
+      for (int e = (part * 256 + threadIdx.x) * 4; e < plane; e += blocks * 1024)
         *reinterpret_cast<f32x4*>(last + e) =
             live && home ? *reinterpret_cast<const f32x4*>(home + e) : f32x4{0.f, 0.f, 0.f, 0.f};
     return;
@@ -615,7 +687,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(ScanArgs a, int plane,
   const float full = power(g2, len), rest = power(g2, L - (int64_t)(n - 1) * len);
   constexpr int AHEAD = 8;  // pieces whose states are in flight together
   const int64_t step = (w.back ? -1 : 1) * (int64_t)a.HV * plane;
-  for (int e = (part * 256 + threadIdx.x) * 4; e < plane; e += parts * 1024) {
+  for (int e = (part * 256 + threadIdx.x) * 4; e < plane; e += blocks * 1024) {
     float* p = w.pieces + ((int64_t)(first + (w.back ? n - 1 : 0)) * a.HV + hv) * plane + e;
     f32x4 s = home ? *reinterpret_cast<const f32x4*>(home + e) : f32x4{0.f, 0.f, 0.f, 0.f};
     for (int i = 0; i < n; i += AHEAD, p += AHEAD * step) {
@@ -658,33 +730,58 @@ __global__ __launch_bounds__(256) void linear_group_sum_kernel(const float* part
   store_vec<4>((blockIdx.y ? out1 : out0) + i, v);
 }
 
-// Tokens of a piece at most, 0: no request is cut. A workgroup's time goes with its tokens, and
-// `slots` of them run at a time, so pieces are sized to fill k rounds of the device, with half a
-// piece more for every request, k = 1 .. 4: more rounds even out pieces of different lengths, fewer
-// spare the joins, which cost what kPieceTokens tokens do.
-constexpr int kPieceTokens = 1000;
-constexpr int64_t kSlots = 512;
-
 int cols_of(int rows) { return rows == 64 ? 64 : 128; }
 
-int cut_of(const LinearShape& s, int rows, int walks) {
+// Tokens of a piece at most, 0: no request is cut. The host knows the number of requests and of their
+// tokens, so the cost of a length l is the mean of two guesses: requests of equal lengths, and one of
+// half the tokens among short ones. In units of the time that a token takes a workgroup that shares
+// its CU with another, seven of which are 4.4 where it is alone:
+//   `units` workgroups of l tokens: 7 l for every 512 of them, and for what is left over 7 l or, up
+//   to 256, 4.4 l; a piece costs `piece` tokens more for its state, which is written, joined and read.
+// Measured, bf16 of 128 x 128, us a call: 4 requests of 4096 tokens, 16 heads: pieces of 256 148,
+// 384 134, 512 117 (the rule's), 768 137, 1024 125, 2048 210, whole requests 326; their gradients:
+// 512 268, 768 266, 1024 246 (the rule's), 1408 296, 2048 291, whole 353; one of 131072: 1024 797, 2048
+// 752, 4160 715 (the rule's). fp32: 4 requests of 2048 tokens, 8 heads: 128 101 (the rule's), 256 90, 512 143,
+// whole 344.
+int64_t cut_of(const LinearShape& s, int rows, int walks) {
   const int64_t blocks = (int64_t)s.HV * (rows / cols_of(rows)) * walks;
-  int64_t best = 0, cost = INT64_MAX;
-  for (int k = 1; k <= 4; ++k) {
-    const int64_t pieces2 = 2 * k * kSlots / blocks - s.B;  // twice the pieces for N tokens
-    if (pieces2 <= 0) continue;
-    const int64_t l = cdiv(cdiv(2 * s.N, pieces2), 64) * 64;
-    if (k * (l + kPieceTokens) < cost) {
-      cost = k * (l + kPieceTokens);
+  const int64_t mean = cdiv(s.N, s.B > 0 ? s.B : 1);
+  if (mean < 16) return 0;  // mostly single tokens, whose states are the cost
+  const int64_t piece = s.bf16 ? 250 : 60;
+  auto rounds = [](int64_t units, double l) {
+    const int64_t left = units % 512;
+    return l * (7. * (double)(units / 512) + (left == 0 ? 0. : left <= 256 ? 4.4 : 7.));
+  };
+  auto cost = [&](int64_t l) {  // l 0: whole requests
+    const int64_t n = l ? cdiv(mean, l) : 1;
+    const double equal = n == 1 ? 1.05 * rounds(s.B * blocks, (double)mean)
+                                : rounds(s.B * n * blocks, (double)(cdiv(cdiv(mean, n), 64) * 64 + piece));
+    if (s.B <= 1) return equal;
+    const double longest = l ? (double)(l + piece) : 0.5 * (double)s.N;
+    const double all = 7. / 512. * (double)blocks *
+                           ((double)s.N + (l ? 1.5 * (double)piece * (double)s.N / (double)l : 0.)) +
+                       2.2 * (double)l;
+    return 0.5 * (equal + (all > 4.4 * longest ? all : 4.4 * longest));
+  };
+  int64_t best = 0;
+  double least = cost(0);
+  auto take = [&](int64_t l) {
+    if (l < 128) l = 128;
+    const double c = l < s.N ? cost(l) : least;
+    if (c < least) {
+      least = c;
       best = l;
     }
-  }
-  if (best < 512) best = best == 0 ? 0 : 512;
-  return best == 0 || s.N <= best ? 0 : (int)best;
+    return l;
+  };
+  for (int64_t n = 1; n <= 64; ++n)
+    if (take(cdiv(cdiv(mean, n), 64) * 64) == 128) break;
+  for (int64_t n = 2; n <= 16; n *= 2) take(cdiv(mean * n, 64) * 64);
+  return best;
 }
 
-int forward_cut(const LinearShape& s) { return cut_of(s, s.dv, 1); }
-int backward_cut(const LinearShape& s) { return cut_of(s, s.dv > s.dk ? s.dv : s.dk, 3); }
+int64_t forward_cut(const LinearShape& s) { return cut_of(s, s.dv, 1); }
+int64_t backward_cut(const LinearShape& s) { return cut_of(s, s.dv > s.dk ? s.dv : s.dk, 3); }
 
 // Requests of at most this many tokens run token by token, where the mean length says that most
 // are and there are enough to fill the device (a call that splits pays a launch for the longer
@@ -695,34 +792,35 @@ int short_tokens(const LinearShape& s) {
 
 // Pieces of cut requests: one of L tokens has at most L / lseg + 1, and each request that is cut has
 // more than lseg tokens, so that there are at most min(B, N / lseg) of them.
-int64_t max_cut(const LinearShape& s, int lseg) {
+int64_t max_cut(const LinearShape& s, int64_t lseg) {
   if (!lseg) return 0;
   const int64_t full = s.N / lseg;
   return full + (s.B < full ? s.B : full);
 }
 
-size_t piece_bytes(const LinearShape& s, int lseg) {
+size_t piece_bytes(const LinearShape& s, int64_t lseg) {
   return align256((size_t)max_cut(s, lseg) * s.HV * s.dv * s.dk * sizeof(float));
 }
 
-int64_t scan_blocks(const ScanArgs& a) {
-  const int64_t segments = a.nreq + (a.lseg ? a.N / a.lseg : 0);
+int64_t scan_blocks(const ScanArgs& a, bool output) {
+  const int64_t segments = output ? a.nreq + (a.lseg ? a.N / a.lseg : 0) : a.max_cut;
   return cdiv(segments * (a.HV / a.rep), 8) * 8 * a.walks * a.rep * a.col_blocks;
 }
 
 // Workgroups of a state in the join: enough to fill the device, few where many requests are likely
 // not cut.
-int join_parts(const LinearShape& s) {
-  int parts = s.dv * s.dk / 1024;
-  while (parts > 1 && s.B * s.HV * (parts / 2) >= 2048) parts /= 2;
-  return parts;
+int join_blocks(const LinearShape& s) {
+  int blocks = s.dv * s.dk / 1024;
+  while (blocks > 1 && s.B * s.HV * (blocks / 2) >= 2048) blocks /= 2;
+  return blocks;
 }
 
 template <typename T, typename TO, int DK, int COLS, bool OUTPUT>
 hipError_t launch_cols(const ScanArgs& a, hipStream_t st) {
   constexpr int CH = sizeof(T) == 4 || DK == 256 ? 32 : 64;
   hipLaunchKernelGGL((linear_scan_kernel<T, TO, DK, CH, COLS, OUTPUT>),
-                     dim3((unsigned)scan_blocks(a)), dim3(kThreads), 0, st, a);
+                     dim3((unsigned)scan_blocks(a, OUTPUT)),
+                     dim3(kThreads<COLS, OUTPUT>), 0, st, a);
   return hipGetLastError();
 }
 
@@ -743,14 +841,14 @@ hipError_t launch_scan(ScanArgs& a, int rows, int dk, hipStream_t st) {
 }
 
 hipError_t launch_join(const LinearShape& s, const ScanArgs& a, hipStream_t st) {
-  const int parts = join_parts(s);
-  hipLaunchKernelGGL(linear_join_kernel, dim3((unsigned)(s.B * s.HV * parts), (unsigned)a.walks),
-                     dim3(256), 0, st, a, s.dv * s.dk, parts);
+  const int blocks = join_blocks(s);
+  hipLaunchKernelGGL(linear_join_kernel, dim3((unsigned)(s.B * s.HV * blocks), (unsigned)a.walks),
+                     dim3(256), 0, st, a, s.dv * s.dk, blocks);
   return hipGetLastError();
 }
 
 ScanArgs scan_args(const LinearShape& s, const float* log_decay, const int64_t* idx,
-                   const int64_t* cu, int lseg) {
+                   const int64_t* cu, int64_t lseg) {
   ScanArgs a{};
   a.log_decay = log_decay;
   a.idx = idx;
@@ -760,7 +858,7 @@ ScanArgs scan_args(const LinearShape& s, const float* log_decay, const int64_t* 
   a.npool = s.pool;
   a.HV = s.HV;
   a.rep = s.HV / s.H;
-  a.lseg = lseg;
+  a.lseg = (int)lseg;
   a.max_cut = (int)max_cut(s, lseg);
   return a;
 }
@@ -792,7 +890,7 @@ hipError_t backward(const LinearShape& s, const void* q, const void* k, const vo
                     const float* log_decay, const float* state, const int64_t* idx,
                     const int64_t* cu, const void* dout, const float* dstate, void* dq, void* dk,
                     void* dv, float* dstate0, char* ws, hipStream_t st) {
-  const int lseg = backward_cut(s);
+  const int64_t lseg = backward_cut(s);
   ScanArgs a = scan_args(s, log_decay, state ? idx : nullptr, cu, lseg);
   const int rep = a.rep;
   const int64_t ldo = (int64_t)s.HV * s.dv;
@@ -839,11 +937,11 @@ hipError_t backward(const LinearShape& s, const void* q, const void* k, const vo
   return hipGetLastError();
 }
 
-bool scan_grids_fit(const LinearShape& s, int lseg, int rows, int walks) {
+bool scan_grids_fit(const LinearShape& s, int64_t lseg, int rows, int walks) {
   ScanArgs a = scan_args(s, nullptr, nullptr, nullptr, lseg);
   a.walks = walks;
   a.col_blocks = rows / cols_of(rows);
-  return grid_ok(scan_blocks(a), kThreads) && grid_ok(s.B * s.HV * join_parts(s), 256);
+  return grid_ok(scan_blocks(a, true), 512) && grid_ok(s.B * s.HV * join_blocks(s), 256);
 }
 
 }  // namespace
@@ -861,7 +959,7 @@ bool linear_prefill_grids_fit(const LinearShape& s) {
 }
 
 bool linear_bwd_grids_fit(const LinearShape& s) {
-  const int lseg = backward_cut(s);
+  const int64_t lseg = backward_cut(s);
   return scan_grids_fit(s, lseg, s.dv, 3) && scan_grids_fit(s, lseg, s.dk, 3) &&
          grid_ok(cdiv(s.N * s.H * s.dk, 1024), 256);
 }
