@@ -1,66 +1,537 @@
 // Low-rank adapters of a batch's requests beside a projection that they share:
 //   out = base + scaling[a] (x A[a]^T) B[a]^T,   a the adapter of the row's request.
-// A workgroup per row: the R sums over K by its waves in turn, then the M outputs.
+//
+// Rows are worked on in tiles of one adapter, whose requests' rows are gathered in order: an adapter
+// is then read once per tile instead of once per request, and a tile of many single tokens is as
+// good as one of a prompt. Two launches:
+//   shrink  x A^T of a tile over a slice of K (fp32), and the tile's rows and adapter, which every
+//           workgroup finds for itself by a scan over the requests;
+//   expand  sums the slices, scales, and adds the product with B^T to base for a range of columns.
+// Both are bound by the bytes of x, base and out: A and B come out of the L2, and the products are
+// R / 16 instructions for every 16 rows and 32 entries. Operands go from memory to registers as the
+// matrix instructions want them (16 bytes a lane: eight bf16 or four fp32 of a row), without LDS.
+//
+// Precision: fp32 sums. bf16: x A^T enters the second product as two bf16 (16 bits), since one would
+// be a rounding of its own; fp32: products of fp32 instructions. base is added in fp32, and the sum
+// rounded once.
 #include "gdn_layer.h"
+#include "gdn_mfma.h"
 
 namespace gdn {
 namespace layer {
 namespace {
 
+using mfma::u32x4;
+typedef mfma::f32x4 acc4;
+
 constexpr int kThreads = 256;
 
+// 16 bytes of a row: lane (r, g) of a wave holds row r, entries 8 g .. 8 g + 7 of 32 (bf16) or
+// 4 g .. 4 g + 3 of 16 (fp32).
 template <typename T>
-__global__ __launch_bounds__(kThreads) void adapter_kernel(AdapterShape s, const T* x,
-                                                           const T* base, const T* A, const T* B,
-                                                           const float* scaling,
-                                                           const int64_t* idx, const int64_t* cu,
-                                                           T* out) {
-  __shared__ float low[128];
-  const int64_t t = blockIdx.x;
-  if (cu && (t < cu[0] || t >= cu[s.B])) return;
-  const int64_t a = idx[cu ? request_of(cu, s.B, t) : t];
-  const bool some = a >= 0 && a < s.adapters;
-  if (some) {
-    for (int r = threadIdx.x >> 6; r < s.R; r += kThreads / 64) {
-      const T* const w = A + (a * s.R + r) * s.K;
-      float sum = 0.f;
-      for (int k = threadIdx.x & 63; k < s.K; k += 64)
-        sum = __builtin_fmaf((float)x[t * s.ldx + k], (float)w[k], sum);
+constexpr int kStep = 64 / (int)sizeof(T);  // entries of a row in one wave's operand
+
+template <typename T>
+__device__ __forceinline__ acc4 mma(u32x4 a, u32x4 b, acc4 c) {
+  if constexpr (sizeof(T) == 2) {
+    return mfma::mma_bf16(__builtin_bit_cast(mfma::bf16x8, a), __builtin_bit_cast(mfma::bf16x8, b),
+                          c);
+  } else {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
 #pragma unroll
-      for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off, 64);
-      if ((threadIdx.x & 63) == 0) low[r] = scaling[a] * sum;
-    }
-  }
-  __syncthreads();
-  for (int m = threadIdx.x; m < s.M; m += kThreads) {
-    float sum = 0.f;
-    if (some)
-      for (int r = 0; r < s.R; ++r)
-        sum = __builtin_fmaf(low[r], (float)B[(a * s.M + m) * s.R + r], sum);
-    out[t * s.ldout + m] = (T)((float)base[t * s.ldbase + m] + sum);
+    for (int i = 0; i < 4; ++i) c = mfma::mma_f32(x[i], y[i], c);
+    return c;
   }
 }
 
-template <typename T>
-hipError_t launch(const AdapterShape& s, const void* x, const void* base, const void* A,
-                  const void* B, const float* scaling, const int64_t* idx, const int64_t* cu,
-                  void* out, hipStream_t st) {
-  hipLaunchKernelGGL(adapter_kernel<T>, dim3((unsigned)s.N), dim3(kThreads), 0, st, s, (const T*)x,
-                     (const T*)base, (const T*)A, (const T*)B, scaling, idx, cu, (T*)out);
+// Entries at .. at + 15 / sizeof(T) of a row of n; zero from n on. VEC: n is a multiple of them and
+// they start on 16 bytes.
+template <typename T, bool VEC>
+__device__ __forceinline__ u32x4 load_row(const T* row, int at, int n) {
+  if constexpr (VEC) {
+    return at < n ? *reinterpret_cast<const u32x4*>(row + at) : u32x4{0, 0, 0, 0};
+  } else {
+    constexpr int V = kVec<T>;
+    typedef T vec_t __attribute__((ext_vector_type(V)));
+    vec_t v;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = at + i < n ? row[at + i] : (T)0.f;
+    return __builtin_bit_cast(u32x4, v);
+  }
+}
+
+struct AdapterArgs {
+  const void *x, *base, *A, *B;
+  const float* scaling;
+  const int64_t *idx, *cu;  // cu NULL: row b belongs to request b
+  void* out;
+  int64_t N, nreq, ldx, ldbase, ldout;
+  int K, M, R, adapters;
+  int tiles, splits, per_split;  // per_split: steps of K in a slice
+  int col_blocks, cols;          // columns of a workgroup in the expansion
+  int* tile_adapter;             // [tiles], -1: no such tile
+  int* tile_rows;                // [tiles][rows of one], -1: none
+  float* low;                    // [splits][tiles][rows][RP]
+};
+
+__device__ __forceinline__ int wave_inclusive(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int y = __shfl_up(v, off, 64);
+    if (lane >= off) v += y;
+  }
+  return v;
+}
+
+// Sum over this thread and those before it in the workgroup, and over all of them.
+__device__ __forceinline__ int block_inclusive(int v, int* s_wave, int& all) {
+  const int wave = threadIdx.x >> 6;
+  v = wave_inclusive(v);
+  __syncthreads();  // s_wave is free
+  if ((threadIdx.x & 63) == 63) s_wave[wave] = v;
+  __syncthreads();
+  int before = 0;
+  all = 0;
+#pragma unroll
+  for (int k = 0; k < kThreads / 64; ++k) {
+    before += k < wave ? s_wave[k] : 0;
+    all += s_wave[k];
+  }
+  return before + v;
+}
+
+// Rows of request b and its adapter (`adapters`: none).
+struct Rows {
+  int begin, count, adapter;
+};
+__device__ __forceinline__ Rows rows_of(const AdapterArgs& a, int64_t b) {
+  Rows r{0, 0, a.adapters};
+  if (b < a.nreq) {
+    int64_t t0 = b, t1 = b + 1;
+    if (a.cu) {
+      t0 = a.cu[b] < 0 ? 0 : a.cu[b];
+      t1 = a.cu[b + 1] < a.N ? a.cu[b + 1] : a.N;
+    }
+    const int64_t k = a.idx[b];
+    r.begin = (int)t0;
+    r.count = t1 > t0 ? (int)(t1 - t0) : 0;
+    r.adapter = k >= 0 && k < a.adapters ? (int)k : a.adapters;
+  }
+  return r;
+}
+
+constexpr int kMaxAdapters = 4096;
+
+// Tile `tile` of the batch: s_rows gets its rows, -1 behind the last. Returns its adapter, `adapters`
+// for rows without one (not tiled where they need no copy), -1 if there are fewer tiles.
+template <int ROWS>
+__device__ int find_tile(const AdapterArgs& a, int tile, int* s_count, int* s_wave, int* s_rows) {
+  __shared__ int s_found[2];
+  const int tid = threadIdx.x;
+  const bool copy = a.base != a.out;
+  const int groups = a.adapters + (copy ? 1 : 0);
+  for (int k = tid; k <= a.adapters; k += kThreads) s_count[k] = 0;
+  if (tid < ROWS) s_rows[tid] = -1;
+  if (tid == 0) s_found[0] = -1;
+  __syncthreads();
+  for (int64_t b = tid; b < a.nreq; b += kThreads) {
+    const Rows r = rows_of(a, b);
+    if (r.count > 0) atomicAdd(&s_count[r.adapter], r.count);  // whole numbers: any order
+  }
+  __syncthreads();
+  // tiles of the groups in front of each; a thread takes a run of them
+  const int run = (groups + kThreads - 1) / kThreads, k0 = tid * run;
+  int mine = 0, all;
+  for (int k = k0; k < k0 + run && k < groups; ++k) mine += (s_count[k] + ROWS - 1) / ROWS;
+  int before = block_inclusive(mine, s_wave, all) - mine;
+  if (tile >= before && tile < before + mine) {
+    for (int k = k0; k < k0 + run; ++k) {
+      const int n = (s_count[k] + ROWS - 1) / ROWS;
+      if (tile < before + n) {
+        s_found[0] = k;
+        s_found[1] = (tile - before) * ROWS;
+        break;
+      }
+      before += n;
+    }
+  }
+  __syncthreads();
+  const int adapter = s_found[0], from = s_found[1];
+  if (adapter < 0) return -1;
+  int seen = 0;  // rows of the adapter in the requests so far
+  for (int64_t base = 0; base < a.nreq && seen < from + ROWS; base += kThreads) {
+    const Rows r = rows_of(a, base + tid);
+    const int n = r.adapter == adapter ? r.count : 0;
+    const int at = seen + block_inclusive(n, s_wave, all) - n;  // of the request's first row
+    const int lo = at > from ? at : from, hi = at + n < from + ROWS ? at + n : from + ROWS;
+    for (int i = lo; i < hi; ++i) s_rows[i - from] = r.begin + (i - at);
+    seen += all;
+  }
+  __syncthreads();
+  return adapter;
+}
+
+// RT tiles of 16 ranks; TT tiles of 16 rows.
+template <typename T, int RT>
+constexpr int kRankPad = RT * 16 < kStep<T> ? kStep<T> : RT * 16;  // ranks of a row of `low`
+
+template <typename T, int TT, int RT, bool VEC>
+__global__ __launch_bounds__(kThreads) void adapter_shrink_kernel(AdapterArgs a) {
+  constexpr int ROWS = 16 * TT, RP = kRankPad<T, RT>, STEP = kStep<T>, LD = RT * 16 + 4;
+  // The waves take turns along K and add up in the end. Of 128 ranks a wave takes half, which
+  // leaves registers for several steps.
+  constexpr int RW = RT == 8 ? 2 : 1, KW = kThreads / 64 / RW, RJ = RT / RW;
+  // steps whose rows are asked for together: enough bytes on their way, as registers allow
+  constexpr int AHEAD = RJ <= 2 ? 4 : 2;
+  constexpr int HALF = KW / 2;  // waves whose sums wait in LDS for those of the others
+  constexpr int kCount = (kMaxAdapters + 1) * 4, kSum = HALF * ROWS * LD * 4;
+  __shared__ __align__(16) char s_mem[kCount > kSum ? kCount : kSum];
+  __shared__ int s_wave[kThreads / 64], s_rows[ROWS];
+  const int tile = blockIdx.x / a.splits, split = blockIdx.x - tile * a.splits;
+  const int adapter = find_tile<ROWS>(a, tile, reinterpret_cast<int*>(s_mem), s_wave, s_rows);
+  if (split == 0) {
+    if (threadIdx.x == 0) a.tile_adapter[tile] = adapter;
+    if (threadIdx.x < ROWS) a.tile_rows[tile * ROWS + threadIdx.x] = s_rows[threadIdx.x];
+  }
+  if (adapter < 0 || adapter >= a.adapters) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const int kw = wave / RW, j0 = wave % RW * RJ;
+  const T *xr[TT], *ar[RJ];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {  // (rows behind the last: the first again)
+    const int row = s_rows[16 * t + r];
+    xr[t] = (const T*)a.x + (int64_t)(row < 0 ? s_rows[0] : row) * a.ldx;
+  }
+#pragma unroll
+  for (int j = 0; j < RJ; ++j) {
+    const int rank = 16 * (j0 + j) + r;
+    ar[j] = (const T*)a.A + ((int64_t)adapter * a.R + (rank < a.R ? rank : 0)) * a.K;
+  }
+  acc4 sum[TT][RJ];
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int j = 0; j < RJ; ++j) sum[t][j] = acc4{0.f, 0.f, 0.f, 0.f};
+  const int steps = (a.K + STEP - 1) / STEP;
+  const int first = split * a.per_split;
+  const int last = first + a.per_split < steps ? first + a.per_split : steps;
+  // Tiles start at different places of the slice: rows lie whole pages apart, and workgroups in step
+  // would ask a few of the memory's channels for all of them.
+  constexpr int TURN = AHEAD * KW;
+  const int turns = (last - first + TURN - 1) / TURN;
+  for (int i = 0, turn = tile % turns; i < turns; ++i, turn = turn + 1 < turns ? turn + 1 : 0) {
+    const int s = first + turn * TURN + AHEAD * kw;
+    u32x4 xf[AHEAD][TT], af[AHEAD][RJ];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int at = s + u < last ? (s + u) * STEP + kVec<T> * g : a.K;
+#pragma unroll
+      for (int t = 0; t < TT; ++t) xf[u][t] = load_row<T, VEC>(xr[t], at, a.K);
+#pragma unroll
+      for (int j = 0; j < RJ; ++j)
+        af[u][j] = load_row<T, VEC>(ar[j], 16 * (j0 + j) + r < a.R ? at : a.K, a.K);
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int j = 0; j < RJ; ++j) sum[t][j] = mma<T>(af[u][j], xf[u][t], sum[t][j]);
+  }
+  // Ranks 16 (j0 + j) + 4 g .. + 3 of row 16 t + r: half of the waves along K leave theirs in LDS for
+  // the other half, until one has the sum.
+  float* const s_sum = reinterpret_cast<float*>(s_mem);
+#pragma unroll
+  for (int n = HALF; n > 0; n /= 2) {
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int j = 0; j < RJ; ++j)
+        if (kw >= n && kw < 2 * n)
+          *reinterpret_cast<acc4*>(s_sum + ((kw - n) * ROWS + 16 * t + r) * LD + 16 * (j0 + j) +
+                                   4 * g) = sum[t][j];
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int j = 0; j < RJ; ++j)
+        if (kw < n)
+          sum[t][j] += *reinterpret_cast<const acc4*>(s_sum + (kw * ROWS + 16 * t + r) * LD +
+                                                      16 * (j0 + j) + 4 * g);
+  }
+  if (kw > 0) return;
+  float* const to = a.low + ((int64_t)split * a.tiles + tile) * (ROWS * RP);
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int j = 0; j < RJ; ++j)
+      *reinterpret_cast<acc4*>(to + (16 * t + r) * RP + 16 * (j0 + j) + 4 * g) = sum[t][j];
+}
+
+// Lanes r and r + 8 of 16 trade a piece: where lane r holds pieces 0 and 1 of row r (16 rows), it gets
+// piece 0 of rows r and r + 8 (r < 8) or piece 1 of rows r - 8 and r, and the other way round.
+__device__ __forceinline__ void trade(u32x4& x0, u32x4& x1, bool low_half) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t give = low_half ? x1[i] : x0[i];
+    const uint32_t get = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, false);
+    x0[i] = low_half ? x0[i] : get;
+    x1[i] = low_half ? get : x1[i];
+  }
+}
+
+template <typename T, int TT, int RT, bool VEC>
+__global__ __launch_bounds__(kThreads) void adapter_expand_kernel(AdapterArgs a) {
+  constexpr int ROWS = 16 * TT, RP = kRankPad<T, RT>, STEP = kStep<T>, KS = RP / STEP;
+  constexpr int V = kVec<T>, NP = sizeof(T) == 2 ? 2 : 1;  // parts of the low-rank rows
+  constexpr int JT = V / 4, COLS = 16 * JT;                // column tiles of a group, its columns
+  constexpr int LD = RP + 16 / (int)sizeof(T);
+  typedef T vec_t __attribute__((ext_vector_type(V)));
+  __shared__ __align__(16) T s_low[NP][ROWS][LD];
+  const int tile = blockIdx.x / a.col_blocks, cb = blockIdx.x - tile * a.col_blocks;
+  const int adapter = a.tile_adapter[tile];
+  if (adapter < 0) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const bool low_half = r < 8;
+  // A wave takes two groups of columns side by side, a line of 128 bytes of 16 rows, and reads and
+  // writes whole lines of eight rows: half lines of sixteen were written back one by one.
+  int row[TT][2];
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) row[t][h] = a.tile_rows[tile * ROWS + 16 * t + 8 * h + (r & 7)];
+  const bool some = adapter < a.adapters;
+  const int begin = cb * a.cols, end = begin + a.cols < a.M ? begin + a.cols : a.M;
+  // Tiles start at different columns, as in the first launch.
+  constexpr int TURN = 2 * COLS * (kThreads / 64);
+  const int turns = (end - begin + TURN - 1) / TURN;
+  int turn = tile % turns, at = 0;  // at: column of the lane's piece of a line
+  u32x4 in[TT][2];
+  auto fetch = [&]() {
+    at = begin + turn * TURN + wave * (2 * COLS) + (low_half ? 0 : COLS) + V * g;
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        in[t][h] = u32x4{0, 0, 0, 0};
+        if (row[t][h] >= 0)
+          in[t][h] =
+              load_row<T, VEC>((const T*)a.base + (int64_t)row[t][h] * a.ldbase, at, a.M);
+      }
+  };
+  fetch();  // on its way while the low-rank rows are summed
+  if (some) {
+    const float scale = a.scaling[adapter];
+    const int64_t slice = (int64_t)a.tiles * (ROWS * RP);
+    constexpr int ITEMS = (ROWS * RP / 4 + kThreads - 1) / kThreads;  // of a thread, four ranks each
+    constexpr int SLICES = ITEMS <= 2 ? 4 : 2;                        // asked for together
+    f32x4 sum[ITEMS];
+#pragma unroll
+    for (int n = 0; n < ITEMS; ++n) sum[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < a.splits; k += SLICES) {
+      f32x4 w[SLICES][ITEMS];
+#pragma unroll
+      for (int u = 0; u < SLICES; ++u)
+#pragma unroll
+        for (int n = 0; n < ITEMS; ++n) {
+          const int i = n * kThreads + threadIdx.x, c = i % (RP / 4) * 4;
+          w[u][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (k + u < a.splits && i < ROWS * RP / 4 && c < RT * 16)
+            w[u][n] = *reinterpret_cast<const f32x4*>(a.low + (k + u) * slice +
+                                                      (int64_t)tile * (ROWS * RP) + 4 * i);
+        }
+#pragma unroll
+      for (int u = 0; u < SLICES; ++u)
+#pragma unroll
+        for (int n = 0; n < ITEMS; ++n) sum[n] += w[u][n];
+    }
+#pragma unroll
+    for (int n = 0; n < ITEMS; ++n) {
+      const int i = n * kThreads + threadIdx.x, lr = i / (RP / 4), c = i % (RP / 4) * 4;
+      if (i >= ROWS * RP / 4) break;
+      const f32x4 v = sum[n] * scale;
+      if constexpr (NP == 1) {
+        *reinterpret_cast<f32x4*>(&s_low[0][lr][c]) = v;
+      } else {
+        bf16x4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float top = __uint_as_float(__float_as_uint(v[e]) & 0xFFFF0000u);
+          hi[e] = __builtin_bit_cast(__bf16, (uint16_t)(__float_as_uint(v[e]) >> 16));
+          lo[e] = (__bf16)(v[e] - top);  // what is cut off
+        }
+        *reinterpret_cast<bf16x4*>(&s_low[0][lr][c]) = hi;
+        *reinterpret_cast<bf16x4*>(&s_low[NP - 1][lr][c]) = lo;
+      }
+    }
+    __syncthreads();
+  }
+  const bool whole_ranks = a.R % V == 0 && ((uintptr_t)a.B & 15) == 0;
+  // Row i of column tile j is column V (i / 4) + 4 j + i % 4 of the group, so that a lane's results
+  // are V neighbouring columns of a row.
+  for (int i = 0; i < turns; ++i) {
+    const int c0 = begin + turn * TURN + wave * (2 * COLS);
+    if (some) {
+      acc4 sum[2][TT][JT];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int j = 0; j < JT; ++j) sum[u][t][j] = acc4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        u32x4 bf[2][JT];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int j = 0; j < JT; ++j) {
+            const int c = c0 + u * COLS + V * (r / 4) + 4 * j + r % 4;
+            const int rank = c < a.M ? STEP * s + V * g : a.R;
+            const T* const br = (const T*)a.B + ((int64_t)adapter * a.M + (c < a.M ? c : 0)) * a.R;
+            bf[u][j] = whole_ranks ? load_row<T, true>(br, rank, a.R)
+                                   : load_row<T, false>(br, rank, a.R);
+          }
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            const u32x4 low =
+                *reinterpret_cast<const u32x4*>(&s_low[p][16 * t + r][STEP * s + V * g]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int j = 0; j < JT; ++j) sum[u][t][j] = mma<T>(bf[u][j], low, sum[u][t][j]);
+          }
+      }
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        trade(in[t][0], in[t][1], low_half);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          vec_t v = __builtin_bit_cast(vec_t, in[t][u]);
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[i] = (T)((float)v[i] + sum[u][t][i / 4][i % 4]);
+          in[t][u] = __builtin_bit_cast(u32x4, v);
+        }
+        trade(in[t][0], in[t][1], low_half);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (row[t][h] < 0) continue;
+        T* const o = (T*)a.out + (int64_t)row[t][h] * a.ldout + at;
+        const vec_t v = __builtin_bit_cast(vec_t, in[t][h]);
+        if constexpr (VEC) {
+          if (at < a.M) *reinterpret_cast<vec_t*>(o) = v;
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (at + i < a.M) o[i] = v[i];
+        }
+      }
+    if (i + 1 < turns) {
+      turn = turn + 1 < turns ? turn + 1 : 0;
+      fetch();
+    }
+  }
+}
+
+// How a call is laid out. Tiles of 64 rows read an adapter a quarter as often as tiles of 16, which
+// leave fewer rows empty where an adapter has few.
+struct Plan {
+  int rows, rank_tiles;  // of a tile
+  int64_t tiles;
+  int splits, per_split, col_blocks, cols;
+  size_t rows_at, low_at, total;
+};
+
+Plan plan_of(const AdapterShape& s) {
+  Plan p;
+  const int64_t groups = s.B < s.adapters + 1 ? s.B : s.adapters + 1;
+  p.rows = s.N >= 48 * groups ? 64 : 16;
+  p.tiles = s.N / p.rows + (groups < s.N ? groups : s.N);
+  p.rank_tiles = s.R <= 16 ? 1 : s.R <= 32 ? 2 : s.R <= 64 ? 4 : 8;
+  const int step = s.bf16 ? 32 : 16, steps = (int)cdiv(s.K, step);
+  // Slices of K: enough workgroups for the device, at least 16 steps each. Every slice of a tile of
+  // many ranks is read again by each of its workgroups in the expansion, so these have fewer (8192
+  // rows, 4096 inputs and outputs, rank 128: 87 us with 256, 116 with 1024; 33860 rows of rank 16: 330
+  // with 1024, 334 with 512, 339 with 4096).
+  int64_t n = cdiv(p.rank_tiles <= 2 ? 1024 : 256, p.tiles);
+  if (n > cdiv(steps, 16)) n = cdiv(steps, 16);
+  p.per_split = (int)cdiv(cdiv(steps, n), 4) * 4;
+  p.splits = (int)cdiv(steps, p.per_split);
+  // Columns of a workgroup: likewise, whole turns of its four waves (33860 rows of rank 16, 8192
+  // outputs: 322 us with 4096 workgroups, 375 with 1024).
+  const int unit = s.bf16 ? 256 : 128;
+  int64_t m = cdiv(p.rank_tiles <= 2 ? 4096 : 1024, p.tiles);
+  if (m > cdiv(s.M, unit)) m = cdiv(s.M, unit);
+  p.cols = (int)(cdiv(cdiv(s.M, m), unit) * unit);
+  p.col_blocks = (int)cdiv(s.M, p.cols);
+  int pad = p.rank_tiles * 16;
+  if (pad < step) pad = step;
+  p.rows_at = align256((size_t)p.tiles * 4);
+  p.low_at = p.rows_at + align256((size_t)p.tiles * p.rows * 4);
+  p.total = p.low_at + align256((size_t)p.splits * p.tiles * p.rows * pad * 4);
+  return p;
+}
+
+template <typename T, int TT, int RT>
+hipError_t launch_tiles(const AdapterArgs& a, bool vec_x, bool vec_out, hipStream_t st) {
+  const auto shrink = vec_x ? adapter_shrink_kernel<T, TT, RT, true>
+                            : adapter_shrink_kernel<T, TT, RT, false>;
+  hipLaunchKernelGGL(shrink, dim3((unsigned)(a.tiles * a.splits)), dim3(kThreads), 0, st, a);
+  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  const auto expand = vec_out ? adapter_expand_kernel<T, TT, RT, true>
+                              : adapter_expand_kernel<T, TT, RT, false>;
+  hipLaunchKernelGGL(expand, dim3((unsigned)(a.tiles * a.col_blocks)), dim3(kThreads), 0, st, a);
   return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch(const AdapterArgs& a, const Plan& p, hipStream_t st) {
+  constexpr int V = kVec<T>;
+  const auto on16 = [](const void* q) { return ((uintptr_t)q & 15) == 0; };
+  const bool vec_x = a.K % V == 0 && a.ldx % V == 0 && on16(a.x) && on16(a.A);
+  const bool vec_out = a.M % V == 0 && a.ldbase % V == 0 && a.ldout % V == 0 && on16(a.base) &&
+                       on16(a.out);
+#define GDN_ADAPTER_CASE(RT)                                                   \
+  if (p.rank_tiles == RT)                                                      \
+    return p.rows == 64 ? launch_tiles<T, 4, RT>(a, vec_x, vec_out, st)        \
+                        : launch_tiles<T, 1, RT>(a, vec_x, vec_out, st);
+  GDN_ADAPTER_CASE(1)
+  GDN_ADAPTER_CASE(2)
+  GDN_ADAPTER_CASE(4)
+  GDN_ADAPTER_CASE(8)
+#undef GDN_ADAPTER_CASE
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t adapter_workspace(const AdapterShape&) { return 0; }
+size_t adapter_workspace(const AdapterShape& s) {
+  return s.N == 0 || s.B == 0 ? 0 : plan_of(s).total;
+}
 
-bool adapter_grids_fit(const AdapterShape& s) { return grid_ok(s.N, kThreads); }
+bool adapter_grids_fit(const AdapterShape& s) {
+  const Plan p = plan_of(s);
+  return p.tiles * p.rows <= 0x7FFFFFFF && grid_ok(p.tiles * p.splits, kThreads) &&
+         grid_ok(p.tiles * p.col_blocks, kThreads);
+}
 
 hipError_t launch_adapter(const AdapterShape& s, const void* x, const void* base, const void* A,
                           const void* B, const float* scaling, const int64_t* idx,
-                          const int64_t* cu, void* out, char*, hipStream_t st) {
-  return s.bf16 ? launch<__bf16>(s, x, base, A, B, scaling, idx, cu, out, st)
-                : launch<float>(s, x, base, A, B, scaling, idx, cu, out, st);
+                          const int64_t* cu, void* out, char* ws, hipStream_t st) {
+  const Plan p = plan_of(s);
+  const AdapterArgs a{x, base, A, B, scaling, idx, cu, out, s.N, s.B, s.ldx, s.ldbase, s.ldout,
+                      s.K, s.M, s.R, s.adapters, (int)p.tiles, p.splits, p.per_split,
+                      p.col_blocks, p.cols, (int*)ws, (int*)(ws + p.rows_at),
+                      (float*)(ws + p.low_at)};
+  return s.bf16 ? launch<__bf16>(a, p, st) : launch<float>(a, p, st);
 }
 
 }  // namespace layer
