@@ -5,17 +5,29 @@ from __future__ import annotations
 import ctypes
 
 from . import GdnAdapterProblem, load_library
-from .layer import _F32, _call, _code, _new, _p, _requests, _rows, _shape, _workspace
+from .layer import _F32, _call, _code, _like, _new, _requests, _rows, _shape, _workspace
+
+
+def _stride(t, name, width, like):
+    """Row stride of t [N, width]: as layer._rows, quick where the rows are plainly fine."""
+    s0, s1 = t.stride()
+    if s1 == 1 and t.dtype is like.dtype and t.get_device() == like.get_device():
+        if t.shape[0] <= 1:
+            return width
+        if s0 >= width:
+            return s0
+    return _rows(t, name, (width,), like)
 
 
 def adapter_problem(x, base, A, batch, out=None) -> GdnAdapterProblem:
     """Descriptor of adapters A [adapters, R, K] on x [N, K] beside base [N, M] (see
     gdn_adapter_problem_t); ``out`` is dense where none is given."""
-    k, m = x.shape[1], base.shape[1]
-    return GdnAdapterProblem(x.shape[0], batch, _rows(x, "x", (k,), x),
-                             _rows(base, "base", (m,), x),
-                             m if out is None else _rows(out, "out", (m,), x), k, m, A.shape[1],
-                             A.shape[0], _code(x, "x"), 0)
+    n, k = x.shape
+    m = base.shape[1]
+    na, r, _ = A.shape
+    return GdnAdapterProblem(n, batch, _stride(x, "x", k, x), _stride(base, "base", m, x),
+                             m if out is None else _stride(out, "out", m, x), k, m, r, na,
+                             _code(x, "x"), 0)
 
 
 def gdn_adapter_workspace_size(prob: GdnAdapterProblem) -> int:
@@ -23,29 +35,36 @@ def gdn_adapter_workspace_size(prob: GdnAdapterProblem) -> int:
 
 
 def _run(what, x, base, A, B, scaling, adapter_indices, cu_seqlens, out, workspace, stream):
-    if x.dim() != 2 or base.dim() != 2 or x.shape[0] != base.shape[0]:
+    if x.dim() != 2 or base.dim() != 2:
         raise ValueError(f"x must be [N, K] and base [N, M], got {list(x.shape)} and "
                          f"{list(base.shape)}")
     if A.dim() != 3:
         raise ValueError(f"A must be [adapters, R, K], got {list(A.shape)}")
-    (n, k), m = x.shape, base.shape[1]
-    na, r = A.shape[:2]
+    n, k = x.shape
+    rows, m = base.shape
+    na, r, _ = A.shape
+    if rows != n:
+        raise ValueError(f"base must have {n} rows, got {rows}")
     _shape(A, "A", (na, r, k), x.dtype, x)
     _shape(B, "B", (na, m, r), x.dtype, x)
     _shape(scaling, "scaling", (na,), _F32, x)
     batch = _requests(adapter_indices, cu_seqlens, x)
     if cu_seqlens is None and batch != n:
         raise ValueError("adapter_indices must have one entry per row of x")
-    if out is None:
-        out = _new(stream, (n, m), x.dtype, x.device)
+    dense = out is None
+    if dense:
+        out = _like(stream, base) if base.is_contiguous() else _new(stream, (n, m), x.dtype, x.device)
     elif out.shape != base.shape:
         raise ValueError(f"out must be {list(base.shape)}, got {list(out.shape)}")
-    prob = adapter_problem(x, base, A, batch, out)
-    ws = _workspace(workspace, gdn_adapter_workspace_size(prob), x.device, stream)
-    fn = getattr(load_library(), what)
-    cu = () if cu_seqlens is None else (_p(cu_seqlens),)
-    _call(what, x.device, stream, fn, _p(x), _p(base), _p(A), _p(B), _p(scaling),
-          _p(adapter_indices), *cu, _p(out), ctypes.byref(prob), _p(ws), ws.numel())
+    prob = adapter_problem(x, base, A, batch, None if dense else out)
+    ref = ctypes.byref(prob)
+    lib = load_library()
+    device = x.device
+    ws = _workspace(workspace, lib.gdn_adapter_workspace_size(ref), device, stream)
+    cu = () if cu_seqlens is None else (cu_seqlens.data_ptr(),)
+    _call(what, device, stream, getattr(lib, what), x.data_ptr(), base.data_ptr(), A.data_ptr(),
+          B.data_ptr(), scaling.data_ptr(), adapter_indices.data_ptr(), *cu, out.data_ptr(), ref,
+          ws.data_ptr(), ws.numel())
     return out
 
 

@@ -400,7 +400,9 @@ gdn_status_t gdn_linear_bwd(const void* q, const void* k, const void* v, const f
   for (const void* p : {q, k, v, dout, (const void*)dq, (const void*)dk, (const void*)dv,
                         (const void*)state_pool, (const void*)dstate, (const void*)dstate0})
     if (!aligned16(p)) return GDN_ERR_INVALID_ARG;
-  if (!linear_bwd_grids_fit(s)) return GDN_ERR_UNSUPPORTED;
+  // rows of dq's and dk's partial sums: 64 of them stay below 2^31 bytes
+  if ((int64_t)s.HV * s.dk > ((int64_t)1 << 22) || !linear_bwd_grids_fit(s))
+    return GDN_ERR_UNSUPPORTED;
   const size_t need = linear_bwd_workspace(s);
   if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255) != 0))
     return GDN_ERR_WORKSPACE;

@@ -746,7 +746,9 @@ int cols_of(int rows) { return rows == 64 ? 64 : 128; }
 int64_t cut_of(const LinearShape& s, int rows, int walks) {
   const int64_t blocks = (int64_t)s.HV * (rows / cols_of(rows)) * walks;
   const int64_t mean = cdiv(s.N, s.B > 0 ? s.B : 1);
-  if (mean < 16) return 0;  // mostly single tokens, whose states are the cost
+  // Mostly single tokens, whose states are the cost; or so many requests that every workgroup would
+  // look for its segment for longer than it may save.
+  if (mean < 16 || s.B > 512) return 0;
   const int64_t piece = s.bf16 ? 250 : 60;
   auto rounds = [](int64_t units, double l) {
     const int64_t left = units % 512;

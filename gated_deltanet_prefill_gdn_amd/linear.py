@@ -8,12 +8,23 @@ from . import GdnLinearProblem, load_library
 from .layer import _F32, _call, _code, _like, _new, _p, _requests, _rows, _shape, _slots, _workspace
 
 
+def _stride(t, name, heads, dim, like):
+    """Token stride of t [N, heads, dim]: as layer._rows, quick where the rows are plainly fine."""
+    s0, s1, s2 = t.stride()
+    if s2 == 1 and s1 == dim and t.dtype is like.dtype and t.get_device() == like.get_device():
+        if t.shape[0] <= 1:
+            return heads * dim
+        if s0 >= heads * dim:
+            return s0
+    return _rows(t, name, (heads, dim), like)
+
+
 def linear_problem(q, k, v, batch, pool_size=0, scale=None) -> GdnLinearProblem:
     """Descriptor of a call on q, k [N, H, dk] and v [N, HV, dv] (see gdn_linear_problem_t)."""
     n, h, dk = q.shape
-    hv, dv = v.shape[1:]
-    return GdnLinearProblem(n, batch, pool_size, _rows(q, "q", (h, dk), v),
-                            _rows(k, "k", (h, dk), v), _rows(v, "v", (hv, dv), v), h, hv, dk, dv,
+    _, hv, dv = v.shape
+    return GdnLinearProblem(n, batch, pool_size, _stride(q, "q", h, dk, v),
+                            _stride(k, "k", h, dk, v), _stride(v, "v", hv, dv, v), h, hv, dk, dv,
                             _code(v, "v"), dk ** -0.5 if scale is None else scale, 0, 0)
 
 
@@ -61,12 +72,15 @@ def gdn_linear_prefill_fwd(q, k, v, log_decay, state_pool, cache_indices, cu_seq
     an optional uint8 device tensor of at least gdn_linear_workspace_size bytes. Rows behind
     cu_seqlens[B], and requests whose cache index is outside the pool, are padding: their outputs
     are not written."""
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens is required")
     prob = _check(q, k, v, log_decay, state_pool, cache_indices, cu_seqlens, scale)
     out = _out(out, v, stream)
-    ws = _workspace(workspace, gdn_linear_workspace_size(prob), v.device, stream)
-    _call("gdn_linear_prefill_fwd", v.device, stream, load_library().gdn_linear_prefill_fwd,
-          _p(q), _p(k), _p(v), _p(log_decay), _p(state_pool), _p(cache_indices), _p(cu_seqlens),
-          _p(out), ctypes.byref(prob), _p(ws), ws.numel())
+    lib, ref, device = load_library(), ctypes.byref(prob), v.device
+    ws = _workspace(workspace, lib.gdn_linear_workspace_size(ref), device, stream)
+    _call("gdn_linear_prefill_fwd", device, stream, lib.gdn_linear_prefill_fwd, q.data_ptr(),
+          k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _p(state_pool), _p(cache_indices),
+          cu_seqlens.data_ptr(), out.data_ptr(), ref, ws.data_ptr(), ws.numel())
     return out
 
 
@@ -75,9 +89,9 @@ def gdn_linear_decode_fwd(q, k, v, log_decay, state_pool, cache_indices, scale=N
     """One step of linear attention, one token per request: row b of every input with request b."""
     prob = _check(q, k, v, log_decay, state_pool, cache_indices, None, scale)
     out = _out(out, v, stream)
-    _call("gdn_linear_decode_fwd", v.device, stream, load_library().gdn_linear_decode_fwd, _p(q),
-          _p(k), _p(v), _p(log_decay), _p(state_pool), _p(cache_indices), _p(out),
-          ctypes.byref(prob))
+    _call("gdn_linear_decode_fwd", v.device, stream, load_library().gdn_linear_decode_fwd,
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state_pool.data_ptr(),
+          cache_indices.data_ptr(), out.data_ptr(), ctypes.byref(prob))
     return out
 
 

@@ -58,6 +58,29 @@ def test_linear_refusals(kind):
             "bwd": lambda: lib.gdn_linear_bwd(*[None] * 15, 0, None)}[kind]() == INV
 
 
+def test_linear_limits():
+    assert linear("bwd", h=1, hv=32768, dk=256, dv=64) == UNS  # rows of the partial sums
+    assert linear("bwd", n=0, b=0, pool=0, nonnull=False, ws=0, ws_ptr=0) == OK
+    # many requests, or hardly more than one token each: none is cut, and nothing has to be kept
+    for n, b in ((513 * 64, 513), (15 * 100, 100), (100, 100), (64, 1)):
+        assert gdn.gdn_linear_workspace_size(prob(n=n, b=b, h=1, hv=1)) == 0, (n, b)
+    assert gdn.gdn_linear_workspace_size(prob(n=100000, b=1, h=1, hv=1)) > 0
+
+
+@pytest.mark.parametrize("kind", ["prefill", "bwd"])
+@pytest.mark.parametrize("dtype", [gdn.GDN_DTYPE_BF16, gdn.GDN_DTYPE_F32])
+def test_linear_workspace_holds_the_states_of_cut_requests_and_no_more(kind, dtype):
+    """Pieces are whole multiples of 64 tokens, at least 128 of them: a piece's state is kept once (and
+    once more for gradients), so the workspace is never above that of pieces of 128 tokens."""
+    size = gdn.gdn_linear_workspace_size if kind == "prefill" else gdn.gdn_linear_bwd_workspace_size
+    for n, b, h, dk, dv in ((131072, 1, 16, 128, 128), (33860, 8, 32, 128, 128), (4096, 1, 2, 256, 64),
+                            (2047, 5, 4, 64, 128), (600, 512, 1, 64, 64), (8192, 512, 4, 64, 64)):
+        state = h * dk * dv * 4
+        most = (n // 128 + min(b, n // 128)) * state * (1 if kind == "prefill" else 2)
+        need = size(prob(n=n, b=b, h=h, hv=h, dk=dk, dv=dv, dtype=dtype))
+        assert need <= most + 512 and need % state < 512, (n, b, need)
+
+
 def test_linear_workspaces_and_empty_calls():
     for kind, size in (("prefill", gdn.gdn_linear_workspace_size), ("bwd", gdn.gdn_linear_bwd_workspace_size)):
         kw = dict(n=100000, b=1)
