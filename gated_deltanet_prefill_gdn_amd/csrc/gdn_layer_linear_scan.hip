@@ -267,6 +267,9 @@ struct Dims {
   static constexpr int AtV = NP * TileK * 2, AtW = AtV + NP * TileV * 2;
   static constexpr int AtQ = AtW + 2 * CH * 4, AtP = AtQ + NP * TileQ * 2;
   static constexpr int Bytes = AtP + PS * TileP * 2;
+  // states: a second pair of tiles for k and v where there is room (bf16), in q's place
+  static constexpr bool Two = sizeof(T) == 2;
+  static constexpr int StateBytes = Two ? AtQ + AtW : AtQ;
   static_assert(AtV % 16 == 0 && AtW % 16 == 0 && AtQ % 16 == 0 && AtP % 16 == 0, "16-byte rows");
 };
 
@@ -284,8 +287,9 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
   constexpr int NS = DK / 16, NKS = DK / 32;   // state tiles, k steps over state entries
   constexpr int TRI = NT == 4 ? 3 : 1;         // tiles of scores for a wave at most
   constexpr int LDQ = D::LDQ, LDK = D::LDK, LDV = D::LDV, LDP = D::LDP;
-  __bf16* const s_k = reinterpret_cast<__bf16*>(lds);
-  __bf16* const s_v = reinterpret_cast<__bf16*>(lds + D::AtV);
+  constexpr bool TWO = !OUT && D::Two;
+  __bf16* s_k = reinterpret_cast<__bf16*>(lds);
+  __bf16* s_v = reinterpret_cast<__bf16*>(lds + D::AtV);
   float* const s_w = reinterpret_cast<float*>(lds + D::AtW);
   __bf16* const s_q = reinterpret_cast<__bf16*>(lds + D::AtQ);
   // decayed scores, row i; entry 32 k + 8 g + e is row j = 32 k + kperm(g, e)
@@ -390,12 +394,26 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
     }
     const int i0 = place(chunk), rows = rows_at(i0);
     const int64_t t0 = token_at(i0);
-    if (chunk > 0) __syncthreads();  // the chunk before has been read
-    qk.template store<NP, true>(s_k, D::TileK, LDK);
-    if constexpr (OUT) qq.template store<NP, false>(s_q, D::TileQ, LDQ);
-    qv.template store<NP, true>(s_v, D::TileV, LDV);
-    __syncthreads();
-    if (chunk + 1 < chunks) fetch(place(chunk + 1));
+    if constexpr (TWO) {  // one barrier a chunk: the next one's tiles are filled beside this one's
+      auto tiles = [&](int n) { return lds + (n & 1 ? D::AtQ : 0); };
+      auto store = [&](int n) {
+        qk.template store<NP, true>(reinterpret_cast<__bf16*>(tiles(n)), D::TileK, LDK);
+        qv.template store<NP, true>(reinterpret_cast<__bf16*>(tiles(n) + D::AtV), D::TileV, LDV);
+        if (n + 1 < chunks) fetch(place(n + 1));
+      };
+      if (chunk == 0) store(0);
+      __syncthreads();
+      if (chunk + 1 < chunks) store(chunk + 1);
+      s_k = reinterpret_cast<__bf16*>(tiles(chunk));
+      s_v = reinterpret_cast<__bf16*>(tiles(chunk) + D::AtV);
+    } else {
+      if (chunk > 0) __syncthreads();  // the chunk before has been read
+      qk.template store<NP, true>(s_k, D::TileK, LDK);
+      if constexpr (OUT) qq.template store<NP, false>(s_q, D::TileQ, LDQ);
+      qv.template store<NP, true>(s_v, D::TileV, LDV);
+      __syncthreads();
+      if (chunk + 1 < chunks) fetch(place(chunk + 1));
+    }
 
     // outputs: the state before decays over the chunk; a piece's state: the chunk's part decays
     // over the rows behind it
@@ -627,7 +645,7 @@ template <typename T, typename TO, int DK, int CH, int COLS, bool OUTPUT>
 __global__ __launch_bounds__((kThreads<COLS, OUTPUT>),
                              (kGroupsPerCU<T, DK, OUTPUT> * kThreads<COLS, OUTPUT> / 256)) void linear_scan_kernel(ScanArgs a) {
   using D = Dims<T, DK, CH, COLS>;
-  __shared__ __align__(16) char lds[OUTPUT ? D::Bytes : D::AtQ];
+  __shared__ __align__(16) char lds[OUTPUT ? D::Bytes : D::StateBytes];
   // Workgroups are dealt to the eight XCDs in turn: the walks, value heads and column blocks that
   // read the same rows go to one of them, one after the other, and find the rows in its L2.
   const int inner = a.walks * a.rep * a.col_blocks;
