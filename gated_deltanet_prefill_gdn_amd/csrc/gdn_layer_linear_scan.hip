@@ -230,20 +230,18 @@ struct Stage {
   }
 };
 
-// The tiles of the lower triangle of NT x NT tiles (row tt, column jt), dealt to the waves so that
-// most of a wave's tiles are of one row: three in rows 3 and 2, (1, 0), (1, 1) and (3, 3), (0, 0);
-// of 32 rows (0, 0), (1, 0) and (1, 1).
+// The tiles of the lower triangle of NT x NT tiles (row tt, column jt), dealt to four waves. Three a
+// wave of 64 rows, the first two of one row of tiles: (3, 0 .. 2), (2, 0 .. 2), (1, 0), (1, 1) and
+// (0, 0); the last wave has (3, 3) three times, which spares a branch. One of 32 rows: (0, 0), (1, 0),
+// (1, 1) twice.
 template <int NT>
-__device__ __forceinline__ bool deal(int wave, int i, int& tt, int& jt) {
+__device__ __forceinline__ void deal(int wave, int i, int& tt, int& jt) {
   if constexpr (NT == 4) {
-    tt = 3 - wave;
-    jt = i;
-    if (wave == 2 && i == 2) tt = jt = 3;
-    return wave < 3 || i == 0;
+    tt = wave == 3 ? 3 : wave == 2 && i == 2 ? 0 : 3 - wave;
+    jt = wave == 3 ? 3 : wave == 2 && i == 2 ? 0 : i;
   } else {
     tt = wave > 0;
     jt = wave > 1;
-    return wave < 3;
   }
 }
 
@@ -358,21 +356,26 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
   };
   fetch(place(0));
 
-  // Decays. Scores: row r of a tile against its columns 4 g + e, on the diagonal and one tile off.
+  // Decays. Scores: of the wave's tiles, row 16 tt + r against its columns 16 jt + 4 g + e, lag - e
+  // rows earlier.
   const Minus minus;
   const double g2 = log2_decay(a.log_decay[hv]);
   const int nlast = len - (chunks - 1) * CH;
-  float on[4], off[4], reach[NT];
-  const float a16 = power(g2, 16), a32 = power(g2, 32);
+  float fade[TRI][4], reach[NT];
+  int tile_q[TRI], tile_k[TRI];
   if constexpr (OUT) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int lag = r - (4 * g + e);
-      on[e] = w.read * w.write * power(g2, lag > 0 ? lag : 0);
-      off[e] = w.read * w.write * power(g2, 16 + lag);
+    for (int i = 0; i < TRI; ++i) {
+      deal<NT>(wv, i, tile_q[i], tile_k[i]);
+      const int lag = 16 * (tile_q[i] - tile_k[i]) + r - 4 * g;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        fade[i][e] = w.read * w.write * power(g2, lag > e ? lag - e : 0);
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) reach[t] = w.read * power(g2, 16 * t + r + 1 - w.back);
+    // the tiles above the diagonal that share a k step with one on it
+    for (int i = tid; i < PS * D::TileP / 2; i += THREADS) reinterpret_cast<uint32_t*>(s_p)[i] = 0;
   }
   // weights in the state's update, of a full chunk and of the last
   if (tid < CH) {
@@ -421,43 +424,42 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
     acc4 y[NT][PT];  // out^T: columns 16 pt + 4 g .. + 3 of row 16 t + r
     if constexpr (OUT) {
       // scores^T, j x i: each wave some of the tiles, decayed
+      acc4 sc[TRI][2];
+#pragma unroll
+      for (int i = 0; i < TRI; ++i) sc[i][0] = sc[i][1] = acc4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < NKS; ++k)
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          bfrag q[TRI];
+#pragma unroll
+          for (int i = 0; i < TRI; ++i) {
+            const u32x2* const qp = reinterpret_cast<const u32x2*>(
+                s_q + p * D::TileQ + (16 * tile_q[i] + r) * LDQ + 32 * k + 8 * g);
+            q[i] = i == 1 ? q[0] : bfrag_of(qp[0], qp[1]);
+          }
+#pragma unroll
+          for (int o = 0; o + p < NP; ++o)
+#pragma unroll
+            for (int i = 0; i < TRI; ++i)
+              sc[i][k % 2] =
+                  mma_bf16(*reinterpret_cast<const bfrag*>(s_k + o * D::TileK +
+                                                           (16 * tile_k[i] + r) * LDK + 32 * k +
+                                                           8 * g),
+                           q[i], sc[i][k % 2]);
+        }
 #pragma unroll
       for (int i = 0; i < TRI; ++i) {
-        int tt, jt;
-        if (!deal<NT>(wv, i, tt, jt)) break;
-        acc4 half[2] = {acc4{0.f, 0.f, 0.f, 0.f}, acc4{0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-        for (int k = 0; k < NKS; ++k)
-#pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            const u32x2* const qp = reinterpret_cast<const u32x2*>(
-                s_q + p * D::TileQ + (16 * tt + r) * LDQ + 32 * k + 8 * g);
-            const bfrag q = bfrag_of(qp[0], qp[1]);
-#pragma unroll
-            for (int o = 0; o + p < NP; ++o)
-              half[k % 2] =
-                  mma_bf16(*reinterpret_cast<const bfrag*>(s_k + o * D::TileK +
-                                                           (16 * jt + r) * LDK + 32 * k + 8 * g),
-                           q, half[k % 2]);
-          }
-        const acc4 sc = half[0] + half[1];
-        __bf16* const to = s_p + (16 * tt + r) * LDP + 32 * (jt / 2) + 8 * g + 4 * (jt % 2);
+        const int lag = 16 * (tile_q[i] - tile_k[i]) + r - 4 * g;
         float v[4];
-        if (jt < tt) {
-          const float far = tt - jt == 1 ? 1.f : tt - jt == 2 ? a16 : a32;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = sc[e] * (off[e] * far);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = 4 * g + e <= r ? sc[e] * on[e] : 0.f;
-          if (jt % 2 == 0)  // the tile beside it shares its k step
-#pragma unroll
-            for (int p = 0; p < PS; ++p)
-              *reinterpret_cast<u32x2*>(to + p * D::TileP + 4) = u32x2{0, 0};
-        }
+        for (int e = 0; e < 4; ++e)
+          v[e] = e <= lag ? (sc[i][0][e] + sc[i][1][e]) * fade[i][e] : 0.f;
         uint32_t lo[PS], hi[PS];
         split_by<PS, F32>(minus, v[0], v[1], lo);
         split_by<PS, F32>(minus, v[2], v[3], hi);
+        __bf16* const to = s_p + (16 * tile_q[i] + r) * LDP + 32 * (tile_k[i] / 2) + 8 * g +
+                           4 * (tile_k[i] % 2);
 #pragma unroll
         for (int p = 0; p < PS; ++p)
           *reinterpret_cast<u32x2*>(to + p * D::TileP) = u32x2{lo[p], hi[p]};
