@@ -1,6 +1,6 @@
 // Internal declarations of the layer operators around the recurrence: short causal
-// convolution, selective state space scan, gated norm, linear attention, low-rank adapters. Not part of the
-// public C ABI.
+// convolution, selective state space scan, gated norm, linear attention, low-rank adapters. Not
+// part of the public C ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -11,19 +11,28 @@
 //   out_i = r a^{i + 1 - b} W q_i + sum_{j <= i} r w a^{i - j} (q_i . k_j) v_j
 //   W    <- a^n W + sum_j (w a^{n - 1 - j + b} v_j) k_j^T
 // all in 16x16x32 matrix instructions with fp32 sums. The decays depend on differences of rows
-// alone: a lane keeps those of a tile on the diagonal and of one beside it in registers.
+// alone, so a lane keeps those of its scores in registers from the first chunk to the last.
 //
-// A workgroup of four waves walks the chunks of one segment of a request for one head and 64 or 128 of W's rows,
-// a quarter of them each, which stay in registers (as columns of W^T) from the first chunk to the last. In
-// the D layout of the products a lane holds four consecutive entries of one column, which is also
-// what the next products want as an operand, so the state and the scores never move between lanes.
+// A workgroup walks the chunks of one segment of a request for one head and 64 or 128 of W's rows,
+// which its waves share out and keep in registers (as columns of W^T). In the D layout of the
+// products a lane holds four consecutive entries of one column, which is also what the next products
+// want as an operand, so the state never moves between lanes; the scores are shared through LDS.
 //
 // Requests longer than a segment are cut into equal pieces: a first launch forms each piece's state
 // from zero (of S, and for gradients of D; their transposes are the same memory), a second joins
 // them in order into the pieces' start states and the final one, and a third forms the outputs of
 // all pieces side by side and takes the requests that are not cut from start to end. A piece's state
 // is summed from its end, and only as far back as weights are not zero in fp32: heads that forget
-// fast stop after a few chunks.
+// fast stop after a few chunks. The three walks of the gradients run side by side in one launch,
+// those of a head and segment on one XCD, whose L2 then holds the rows that they share (4 x 4096
+// tokens, 16 heads: 474 MB read, of 604 that the walks ask for).
+//
+// What bounds it (bf16, 128 x 128): a chunk's products and the vector work between them, 164 matrix
+// and 590 vector instructions a wave. One request of 131072 tokens, 16 heads, 712 us a call: outputs
+// 490 us at 4.4 TB/s, matrix cores busy 36 % and vector units 42 % of the time, two workgroups a CU;
+// states 215 at 2.7 (the slow heads' columns lie side by side in a row and do not reach every memory
+// channel: 4.0 TB/s where all heads are slow), join 25. 8 ragged requests of 33860 tokens, 32 heads,
+// 420 us (286, 132 and 20). Gradients of 4 x 4096 tokens, 16 heads, 250 us (177, 64 and 17).
 //
 // Precision: bf16 inputs enter the products as they are. The decayed v of the state's update are
 // three bf16 (24 bits), since states are fp32 results. What only outputs take, which end as bf16, is
@@ -40,8 +49,8 @@ namespace {
 using mfma::kperm;
 using mfma::mma_bf16;
 
-// -1 beside either half of a register of two bf16. (Kept in registers: as literals they are taken
-// for something else.)
+// -1 beside either half of a register of two bf16. (Kept in registers: as a literal operand of the
+// two-term product they give other results.)
 struct Minus {
   uint32_t lo = 0x0000BF80u, hi = 0xBF800000u;
   __device__ __forceinline__ Minus() { asm("" : "+v"(lo), "+v"(hi)); }
@@ -639,13 +648,14 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const Walk& w, c
 }
 
 // Workgroups of a CU that the registers are held to (fp32: LDS for one at 128 and more).
-template <typename T, int DK, bool OUTPUT>
+template <typename T>
 constexpr int kGroupsPerCU = sizeof(T) == 4 ? 1 : 2;
 
 // The pieces' states (OUTPUT false); the outputs of pieces, and whole requests.
 template <typename T, typename TO, int DK, int CH, int COLS, bool OUTPUT>
 __global__ __launch_bounds__((kThreads<COLS, OUTPUT>),
-                             (kGroupsPerCU<T, DK, OUTPUT> * kThreads<COLS, OUTPUT> / 256)) void linear_scan_kernel(ScanArgs a) {
+                             (kGroupsPerCU<T> * kThreads<COLS, OUTPUT> / 256))
+void linear_scan_kernel(ScanArgs a) {
   using D = Dims<T, DK, CH, COLS>;
   __shared__ __align__(16) char lds[OUTPUT ? D::Bytes : D::StateBytes];
   // Workgroups are dealt to the eight XCDs in turn: the walks, value heads and column blocks that
@@ -758,11 +768,11 @@ int cols_of(int rows) { return rows == 64 ? 64 : 128; }
 // its CU with another, seven of which are 4.4 where it is alone:
 //   `units` workgroups of l tokens: 7 l for every 512 of them, and for what is left over 7 l or, up
 //   to 256, 4.4 l; a piece costs `piece` tokens more for its state, which is written, joined and read.
-// Measured, bf16 of 128 x 128, us a call: 4 requests of 4096 tokens, 16 heads: pieces of 256 148,
-// 384 134, 512 117 (the rule's), 768 137, 1024 125, 2048 210, whole requests 326; their gradients:
-// 512 268, 768 266, 1024 246 (the rule's), 1408 296, 2048 291, whole 353; one of 131072: 1024 797, 2048
-// 752, 4160 715 (the rule's). fp32: 4 requests of 2048 tokens, 8 heads: 128 101 (the rule's), 256 90, 512 143,
-// whole 344.
+// Measured, bf16 of 128 x 128, us a call (* the rule's): 4 requests of 4096 tokens, 16 heads: pieces
+// of 128 196, 256 147, 384 135, 512* 117, 768 134, 1024 119, 2048 199, whole requests 314; their
+// gradients: 512 264, 768 264, 1024* 241, 1408 288, 2048 277, whole 335; one of 131072: 512 924, 1024
+// 818, 2048 760, 4096* 711; one of 4096: 128 61, 256* 54, 512 66, 1024 104, whole 297. fp32, 4 requests
+// of 2048 tokens, 8 heads: 128* 103, 256 92, 512 141, whole 336.
 int64_t cut_of(const LinearShape& s, int rows, int walks) {
   const int64_t blocks = (int64_t)s.HV * (rows / cols_of(rows)) * walks;
   const int64_t mean = cdiv(s.N, s.B > 0 ? s.B : 1);

@@ -529,9 +529,10 @@ gdn_status_t gdn_linear_decode_fwd(const void* q, const void* k, const void* v,
  *   dstate0 [B, HV, dv, dk] fp32: gradient of each request's start state; NULL to skip
  * All overwritten (dq, dk and dv on requests' rows). A non-finite k also reaches that column of dq
  * up to 31 tokens before it, a non-finite q or dout that column of dk or dv up to 31 behind it. A
- * request without tokens has dstate0 =
- * dstate, a padding request zero. Precision as for the forward call: bf16 gradients are rounded
- * once, dstate0 keeps 24 bits. All pointers but cu_seqlens and cache_indices 16-byte aligned.
+ * request without tokens has dstate0 = dstate, a padding request zero. Precision as for the forward
+ * call: bf16 gradients are rounded once, dstate0 keeps 24 bits. All pointers but cu_seqlens,
+ * cache_indices and log_decay 16-byte aligned. Where value heads share q and k the workspace holds
+ * their fp32 parts of dq and dk: 8 N HV dk bytes.
  * workspace: at least gdn_linear_bwd_workspace_size bytes, 256-byte aligned. */
 size_t gdn_linear_bwd_workspace_size(const gdn_linear_problem_t* prob);
 gdn_status_t gdn_linear_bwd(const void* q, const void* k, const void* v, const float* log_decay,
@@ -566,8 +567,10 @@ typedef struct {
  *   adapter_indices [B] int64: any number of requests may share an adapter
  *   cu_seqlens [B + 1]
  * fp32 sums; x A^T is held in fp32 and enters the second product with 16 bits (bf16) or 24 bits
- * (fp32); the sum with base is rounded once. Vectors of 16 bytes where pointers, strides and sizes
- * allow it, else element by element. Rows from cu_seqlens[B] on are not written.
+ * (fp32); the sum with base is rounded once. A non-finite x, or a sum past fp32's range, reaches its
+ * own row alone, where an infinite value may stand as NaN. Vectors of 16 bytes where pointers, strides
+ * and sizes allow it, else element by element. Rows from cu_seqlens[B] on are not written. Every
+ * workgroup looks through the B requests: thousands of them cost some 3 us a thousand.
  * workspace: at least gdn_adapter_workspace_size bytes, 256-byte aligned. */
 size_t gdn_adapter_workspace_size(const gdn_adapter_problem_t* prob);
 gdn_status_t gdn_adapter_fwd(const void* x, const void* base, const void* A, const void* B,
