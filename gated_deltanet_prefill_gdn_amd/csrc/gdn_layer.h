@@ -193,7 +193,10 @@ struct LinearShape {
   int H, HV, dk, dv;
   bool bf16;
   float scale;
+  int64_t cut;  // linear_cut's, of the direction
 };
+// Tokens of the pieces that long requests are cut into, 0: none is cut.
+int64_t linear_cut(const LinearShape& s, bool backward);
 size_t linear_workspace(const LinearShape& s);
 size_t linear_bwd_workspace(const LinearShape& s);
 bool linear_prefill_grids_fit(const LinearShape& s);

@@ -135,7 +135,7 @@ gdn_status_t check_linear(const gdn_linear_problem_t* p, LinearShape* s) {
     return GDN_ERR_UNSUPPORTED;
   *s = LinearShape{p->total_tokens, p->batch,        p->pool_size,   p->q_stride, p->k_stride,
                    p->v_stride,     p->num_qk_heads, p->num_v_heads, p->head_k,   p->head_v,
-                   p->dtype == GDN_DTYPE_BF16,       p->scale};
+                   p->dtype == GDN_DTYPE_BF16,       p->scale,         0};
   const int v = vec(s->bf16);
   const int64_t qk = (int64_t)s->H * s->dk, vv = (int64_t)s->HV * s->dv;
   if (s->ldq < qk || s->ldk < qk || s->ldv < vv) return GDN_ERR_INVALID_ARG;
@@ -334,7 +334,9 @@ gdn_status_t gdn_norm_bwd(const void* x, const float* weight, const float* bias,
 
 size_t gdn_linear_workspace_size(const gdn_linear_problem_t* prob) {
   LinearShape s;
-  return check_linear(prob, &s) == GDN_OK ? linear_workspace(s) : 0;
+  if (check_linear(prob, &s) != GDN_OK) return 0;
+  s.cut = linear_cut(s, false);
+  return linear_workspace(s);
 }
 
 gdn_status_t gdn_linear_prefill_fwd(const void* q, const void* k, const void* v,
@@ -350,6 +352,7 @@ gdn_status_t gdn_linear_prefill_fwd(const void* q, const void* k, const void* v,
   if (state_pool && (!cache_indices || s.pool < 1)) return GDN_ERR_INVALID_ARG;
   for (const void* p : {q, k, v, (const void*)out, (const void*)state_pool})
     if (!aligned16(p)) return GDN_ERR_INVALID_ARG;
+  s.cut = linear_cut(s, false);
   if (!linear_prefill_grids_fit(s)) return GDN_ERR_UNSUPPORTED;
   const size_t need = linear_workspace(s);
   if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255) != 0))
@@ -381,7 +384,9 @@ gdn_status_t gdn_linear_decode_fwd(const void* q, const void* k, const void* v,
 
 size_t gdn_linear_bwd_workspace_size(const gdn_linear_problem_t* prob) {
   LinearShape s;
-  return check_linear(prob, &s) == GDN_OK ? linear_bwd_workspace(s) : 0;
+  if (check_linear(prob, &s) != GDN_OK) return 0;
+  s.cut = linear_cut(s, true);
+  return linear_bwd_workspace(s);
 }
 
 gdn_status_t gdn_linear_bwd(const void* q, const void* k, const void* v, const float* log_decay,
@@ -400,6 +405,7 @@ gdn_status_t gdn_linear_bwd(const void* q, const void* k, const void* v, const f
   for (const void* p : {q, k, v, dout, (const void*)dq, (const void*)dk, (const void*)dv,
                         (const void*)state_pool, (const void*)dstate, (const void*)dstate0})
     if (!aligned16(p)) return GDN_ERR_INVALID_ARG;
+  s.cut = linear_cut(s, true);
   // rows of dq's and dk's partial sums: 64 of them stay below 2^31 bytes
   if ((int64_t)s.HV * s.dk > ((int64_t)1 << 22) || !linear_bwd_grids_fit(s))
     return GDN_ERR_UNSUPPORTED;

@@ -762,58 +762,94 @@ __global__ __launch_bounds__(256) void linear_group_sum_kernel(const float* part
 
 int cols_of(int rows) { return rows == 64 ? 64 : 128; }
 
+// A launch of the walks as the rule below sees it: workgroups for a segment, microseconds that one of
+// them takes for a token on a CU of its own, and whether it fills the CU.
+struct Work {
+  int64_t groups;
+  double token;
+  bool fills;
+};
+
+// W of rows x dk, `heads` of it. Measured, ns a token of 256 workgroups: bf16 64 x 64 42, 128 x 128
+// 106, 128 x 256 157; fp32 96, 221 and 362; 512 take 1.65 times as long, or twice.
+Work work_of(const LinearShape& s, int64_t heads, int dk, int rows) {
+  const int cols = cols_of(rows);
+  return Work{heads * (rows / cols), 0.1 * (dk + 32) * (cols + 32) / 25600. * (s.bf16 ? 1. : 2.1),
+              !s.bf16 && dk * cols >= 128 * 128};
+}
+
+// Microseconds of a token of `groups` workgroups: in rounds of 512, two on a CU, and what is left over.
+double rounds(int64_t groups, const Work& w) {
+  const auto rest = [&](int64_t n) {
+    return n == 0 ? 0. : n > 256 ? 1.65 * w.token : w.token * (0.65 + 0.35 * (double)n / 256.);
+  };
+  return w.fills ? w.token * (double)(groups / 256) + rest(groups % 256)
+                 : 1.65 * w.token * (double)(groups / 512) + rest(groups % 512);
+}
+
 // Tokens of a piece at most, 0: no request is cut. The host knows the number of requests and of their
-// tokens, so the cost of a length l is the mean of two guesses: requests of equal lengths, and one of
-// half the tokens among short ones. In units of the time that a token takes a workgroup that shares
-// its CU with another, seven of which are 4.4 where it is alone:
-//   `units` workgroups of l tokens: 7 l for every 512 of them, and for what is left over 7 l or, up
-//   to 256, 4.4 l; a piece costs `piece` tokens more for its state, which is written, joined and read.
+// tokens alone, so the time of a length is the mean of two guesses: requests of equal lengths, and one
+// of half the tokens among short ones. Cutting costs a pass for the states (a sixth of the time of the
+// outputs, fp32 0.4, if no head forgets), two launches more, and the pieces' states, which are written,
+// joined (read, written) and read.
 // Measured, bf16 of 128 x 128, us a call (* the rule's): 4 requests of 4096 tokens, 16 heads: pieces
 // of 128 196, 256 147, 384 135, 512* 117, 768 134, 1024 119, 2048 199, whole requests 314; their
 // gradients: 512 264, 768 264, 1024* 241, 1408 288, 2048 277, whole 335; one of 131072: 512 924, 1024
 // 818, 2048 760, 4096* 711; one of 4096: 128 61, 256* 54, 512 66, 1024 104, whole 297. fp32, 4 requests
-// of 2048 tokens, 8 heads: 128* 103, 256 92, 512 141, whole 336.
-int64_t cut_of(const LinearShape& s, int rows, int walks) {
-  const int64_t blocks = (int64_t)s.HV * (rows / cols_of(rows)) * walks;
-  const int64_t mean = cdiv(s.N, s.B > 0 ? s.B : 1);
+// of 2048 tokens, 8 heads: 128 103, 256* 92, 512 141, whole 336.
+int64_t cut_of(const LinearShape& s, bool backward) {
+  const int64_t mean = cdiv(s.N, s.B > 0 ? s.B : 1), half = s.N / 2;
   // Mostly single tokens, whose states are the cost; or so many requests that every workgroup would
   // look for its segment for longer than it may save.
   if (mean < 16 || s.B > 512) return 0;
-  const int64_t piece = s.bf16 ? 250 : 60;
-  auto rounds = [](int64_t units, double l) {
-    const int64_t left = units % 512;
-    return l * (7. * (double)(units / 512) + (left == 0 ? 0. : left <= 256 ? 4.4 : 7.));
-  };
+  Work launches[2] = {work_of(s, s.HV, s.dk, s.dv), Work{0, 0., false}};
+  Work states = launches[0];
+  states.token *= s.bf16 ? 0.15 : 0.4;
+  states.fills = false;
+  if (backward) {
+    states.groups *= 2;
+    if (s.dk == s.dv && s.HV == s.H)
+      launches[0].groups *= 3;
+    else
+      launches[1] = work_of(s, 2 * s.HV, s.dv, s.dk);
+  }
+  constexpr double kBytes = 5e6, kLaunches = 4., kCut = 12.;  // a microsecond's bytes; microseconds
+  const double piece = 16. * s.HV * s.dk * s.dv * (backward ? 2. : 1.) / kBytes;
   auto cost = [&](int64_t l) {  // l 0: whole requests
-    const int64_t n = l ? cdiv(mean, l) : 1;
-    const double equal = n == 1 ? 1.05 * rounds(s.B * blocks, (double)mean)
-                                : rounds(s.B * n * blocks, (double)(cdiv(cdiv(mean, n), 64) * 64 + piece));
+    const bool cut = l > 0 && l < mean, cut_half = l > 0 && l < half;
+    const int64_t n = cut ? cdiv(mean, l) : 1, of = n > 1 ? cdiv(cdiv(mean, n), 64) * 64 : mean;
+    double equal = 0., work = 0., chain = 0.;
+    for (const Work& w : launches) {
+      equal += rounds(s.B * n * w.groups, w) * (double)of;
+      work += (double)(s.N * w.groups) * w.token * (w.fills ? 1. : 0.82) / 256.;
+      chain += w.token * (double)(cut_half ? l : half);
+    }
+    if (cut)
+      equal += rounds(s.B * n * states.groups, states) * (double)of + kCut + (double)(s.B * n) * piece;
+    else if (l)
+      equal += kLaunches;
     if (s.B <= 1) return equal;
-    const double longest = l ? (double)(l + piece) : 0.5 * (double)s.N;
-    const double all = 7. / 512. * (double)blocks *
-                           ((double)s.N + (l ? 1.5 * (double)piece * (double)s.N / (double)l : 0.)) +
-                       2.2 * (double)l;
-    return 0.5 * (equal + (all > 4.4 * longest ? all : 4.4 * longest));
+    if (cut_half) {
+      work += (double)(s.N * states.groups) * states.token * 0.82 / 256.;
+      chain += states.token * (double)l;
+    }
+    const double ragged = (work + 0.5 * chain > chain ? work + 0.5 * chain : chain) +
+                          (cut_half ? kCut + 1.5 * (double)s.N / (double)l * piece : l ? kLaunches : 0.);
+    return 0.5 * (equal + ragged);
   };
   int64_t best = 0;
   double least = cost(0);
   auto take = [&](int64_t l) {
-    if (l < 128) l = 128;
-    const double c = l < s.N ? cost(l) : least;
+    const double c = l >= 128 && l < s.N ? cost(l) : least;
     if (c < least) {
       least = c;
       best = l;
     }
-    return l;
   };
-  for (int64_t n = 1; n <= 64; ++n)
-    if (take(cdiv(cdiv(mean, n), 64) * 64) == 128) break;
-  for (int64_t n = 2; n <= 16; n *= 2) take(cdiv(mean * n, 64) * 64);
+  for (int64_t l = 128; l < s.N && l <= 16 * mean; l += cdiv(l, 4 * 64) * 64) take(l);
+  for (int64_t n = 1; n <= 64; ++n) take(cdiv(cdiv(mean, n), 64) * 64);
   return best;
 }
-
-int64_t forward_cut(const LinearShape& s) { return cut_of(s, s.dv, 1); }
-int64_t backward_cut(const LinearShape& s) { return cut_of(s, s.dv > s.dk ? s.dv : s.dk, 3); }
 
 // Requests of at most this many tokens run token by token, where the mean length says that most
 // are and there are enough to fill the device (a call that splits pays a launch for the longer
@@ -902,7 +938,7 @@ template <typename T>
 hipError_t forward(const LinearShape& s, const void* q, const void* k, const void* v,
                    const float* log_decay, float* state, const int64_t* idx, const int64_t* cu,
                    void* out, char* ws, hipStream_t st) {
-  ScanArgs a = scan_args(s, log_decay, state ? idx : nullptr, cu, forward_cut(s));
+  ScanArgs a = scan_args(s, log_decay, state ? idx : nullptr, cu, s.cut);
   const int rep = a.rep;
   a.short_len = short_tokens(s);
   if (a.short_len)
@@ -922,7 +958,7 @@ hipError_t backward(const LinearShape& s, const void* q, const void* k, const vo
                     const float* log_decay, const float* state, const int64_t* idx,
                     const int64_t* cu, const void* dout, const float* dstate, void* dq, void* dk,
                     void* dv, float* dstate0, char* ws, hipStream_t st) {
-  const int64_t lseg = backward_cut(s);
+  const int64_t lseg = s.cut;
   ScanArgs a = scan_args(s, log_decay, state ? idx : nullptr, cu, lseg);
   const int rep = a.rep;
   const int64_t ldo = (int64_t)s.HV * s.dv;
@@ -978,21 +1014,22 @@ bool scan_grids_fit(const LinearShape& s, int64_t lseg, int rows, int walks) {
 
 }  // namespace
 
-size_t linear_workspace(const LinearShape& s) { return piece_bytes(s, forward_cut(s)); }
+int64_t linear_cut(const LinearShape& s, bool backward) { return cut_of(s, backward); }
+
+size_t linear_workspace(const LinearShape& s) { return piece_bytes(s, s.cut); }
 
 size_t linear_bwd_workspace(const LinearShape& s) {
-  return 2 * piece_bytes(s, backward_cut(s)) +
+  return 2 * piece_bytes(s, s.cut) +
          (s.HV > s.H ? align256(2 * sizeof(float) * s.N * s.HV * s.dk) : 0);
 }
 
 bool linear_prefill_grids_fit(const LinearShape& s) {
-  return scan_grids_fit(s, forward_cut(s), s.dv, 1) &&
+  return scan_grids_fit(s, s.cut, s.dv, 1) &&
          (!short_tokens(s) || linear_token_grid_fits(s));
 }
 
 bool linear_bwd_grids_fit(const LinearShape& s) {
-  const int64_t lseg = backward_cut(s);
-  return scan_grids_fit(s, lseg, s.dv, 3) && scan_grids_fit(s, lseg, s.dk, 3) &&
+  return scan_grids_fit(s, s.cut, s.dv, 3) && scan_grids_fit(s, s.cut, s.dk, 3) &&
          grid_ok(cdiv(s.N * s.H * s.dk, 1024), 256);
 }
 
