@@ -50,19 +50,38 @@ __device__ __forceinline__ acc4 mma(u32x4 a, u32x4 b, acc4 c) {
 }
 
 // Entries at .. at + 15 / sizeof(T) of a row of n; zero from n on. VEC: n is a multiple of them and
-// they start on 16 bytes.
+// they start on 16 bytes. Otherwise they start anywhere, which the memory system takes as well; where
+// they would end behind the row its last 16 bytes are read, and end_of_row() moves them into place
+// when they have arrived (8192 rows of 4095 inputs and outputs, rank 16: 128 us, 162 with every entry
+// by itself; 69 for 4096, whose rows start on 16 bytes).
 template <typename T, bool VEC>
 __device__ __forceinline__ u32x4 load_row(const T* row, int at, int n) {
+  constexpr int V = kVec<T>;
   if constexpr (VEC) {
     return at < n ? *reinterpret_cast<const u32x4*>(row + at) : u32x4{0, 0, 0, 0};
   } else {
-    constexpr int V = kVec<T>;
-    typedef T vec_t __attribute__((ext_vector_type(V)));
-    vec_t v;
+    u32x4 v;
+    if (n >= V) {
+      __builtin_memcpy(&v, row + (at < n - V ? at : n - V), 16);
+    } else {
+      typedef T vec_t __attribute__((ext_vector_type(V)));
+      vec_t t;
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = at + i < n ? row[at + i] : (T)0.f;
-    return __builtin_bit_cast(u32x4, v);
+      for (int i = 0; i < V; ++i) t[i] = at + i < n ? row[at + i] : (T)0.f;
+      v = __builtin_bit_cast(u32x4, t);
+    }
+    return v;
   }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ bool ends_row(int at, int n) {
+  return !VEC && n >= kVec<T> && at > n - kVec<T>;
+}
+template <typename T>
+__device__ __forceinline__ u32x4 end_of_row(u32x4 v, int at, int n) {
+  const int beyond = (at + kVec<T> - n) * (int)sizeof(T);  // bytes
+  const unsigned __int128 x = __builtin_bit_cast(unsigned __int128, v) >> (8 * (beyond & 15));
+  return beyond < 16 ? __builtin_bit_cast(u32x4, x) : u32x4{0, 0, 0, 0};
 }
 
 struct AdapterArgs {
@@ -209,7 +228,7 @@ __global__ __launch_bounds__(kThreads) void adapter_shrink_kernel(AdapterArgs a)
     xr[t] = (const T*)a.x + (int64_t)(row < 0 ? s_rows[0] : row) * a.ldx;
   }
 #pragma unroll
-  for (int j = 0; j < RJ; ++j) {
+  for (int j = 0; j < RJ; ++j) {  // (behind the last rank the first again: B is taken as zero there)
     const int rank = 16 * (j0 + j) + r;
     ar[j] = (const T*)a.A + ((int64_t)adapter * a.R + (rank < a.R ? rank : 0)) * a.K;
   }
@@ -227,15 +246,46 @@ __global__ __launch_bounds__(kThreads) void adapter_shrink_kernel(AdapterArgs a)
   const int turns = (last - first + TURN - 1) / TURN;
   for (int i = 0, turn = tile % turns; i < turns; ++i, turn = turn + 1 < turns ? turn + 1 : 0) {
     const int s = first + turn * TURN + AHEAD * kw;
+    const auto place = [&](int u) { return s + u < last ? (s + u) * STEP + kVec<T> * g : a.K; };
+    if constexpr (!VEC) {
+      if (s + AHEAD > last || (s + AHEAD) * STEP > a.K) {  // to the end of the rows: step by step
+#pragma unroll 1
+        for (int u = 0; u < AHEAD && s + u < last; ++u) {
+          const int at = place(u);
+          u32x4 xe[TT], ae[RJ];
+#pragma unroll
+          for (int t = 0; t < TT; ++t) xe[t] = load_row<T, false>(xr[t], at, a.K);
+#pragma unroll
+          for (int j = 0; j < RJ; ++j) ae[j] = load_row<T, false>(ar[j], at, a.K);
+          if (ends_row<T, false>(at, a.K)) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) xe[t] = end_of_row<T>(xe[t], at, a.K);
+#pragma unroll
+            for (int j = 0; j < RJ; ++j) ae[j] = end_of_row<T>(ae[j], at, a.K);
+          }
+#pragma unroll
+          for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int j = 0; j < RJ; ++j) sum[t][j] = mma<T>(ae[j], xe[t], sum[t][j]);
+        }
+        continue;
+      }
+    }
+    const auto load = [&](const T* row, int u) {
+      u32x4 v;
+      if constexpr (VEC)
+        v = load_row<T, true>(row, place(u), a.K);
+      else
+        __builtin_memcpy(&v, row + (s + u) * STEP + kVec<T> * g, 16);
+      return v;
+    };
     u32x4 xf[AHEAD][TT], af[AHEAD][RJ];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
-      const int at = s + u < last ? (s + u) * STEP + kVec<T> * g : a.K;
 #pragma unroll
-      for (int t = 0; t < TT; ++t) xf[u][t] = load_row<T, VEC>(xr[t], at, a.K);
+      for (int t = 0; t < TT; ++t) xf[u][t] = load(xr[t], u);
 #pragma unroll
-      for (int j = 0; j < RJ; ++j)
-        af[u][j] = load_row<T, VEC>(ar[j], 16 * (j0 + j) + r < a.R ? at : a.K, a.K);
+      for (int j = 0; j < RJ; ++j) af[u][j] = load(ar[j], u);
     }
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u)
@@ -373,11 +423,16 @@ __global__ __launch_bounds__(kThreads) void adapter_expand_kernel(AdapterArgs a)
     }
     __syncthreads();
   }
-  const bool whole_ranks = a.R % V == 0 && ((uintptr_t)a.B & 15) == 0;
   // Row i of column tile j is column V (i / 4) + 4 j + i % 4 of the group, so that a lane's results
   // are V neighbouring columns of a row.
   for (int i = 0; i < turns; ++i) {
     const int c0 = begin + turn * TURN + wave * (2 * COLS);
+    if (ends_row<T, VEC>(at, a.M)) {
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) in[t][h] = end_of_row<T>(in[t][h], at, a.M);
+    }
     if (some) {
       acc4 sum[2][TT][JT];
 #pragma unroll
@@ -389,16 +444,25 @@ __global__ __launch_bounds__(kThreads) void adapter_expand_kernel(AdapterArgs a)
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         u32x4 bf[2][JT];
+        const auto column = [&](int u, int j) { return c0 + u * COLS + V * (r / 4) + 4 * j + r % 4; };
+        const auto rank = [&](int c) { return c < a.M ? STEP * s + V * g : a.R; };
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int j = 0; j < JT; ++j) {
-            const int c = c0 + u * COLS + V * (r / 4) + 4 * j + r % 4;
-            const int rank = c < a.M ? STEP * s + V * g : a.R;
+            const int c = column(u, j);
             const T* const br = (const T*)a.B + ((int64_t)adapter * a.M + (c < a.M ? c : 0)) * a.R;
-            bf[u][j] = whole_ranks ? load_row<T, true>(br, rank, a.R)
-                                   : load_row<T, false>(br, rank, a.R);
+            bf[u][j] = load_row<T, VEC>(br, rank(c), a.R);
           }
+        if constexpr (!VEC) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < JT; ++j) {
+              const int at = rank(column(u, j));
+              if (ends_row<T, VEC>(at, a.R)) bf[u][j] = end_of_row<T>(bf[u][j], at, a.R);
+            }
+        }
 #pragma unroll
         for (int p = 0; p < NP; ++p)
 #pragma unroll
@@ -433,6 +497,8 @@ __global__ __launch_bounds__(kThreads) void adapter_expand_kernel(AdapterArgs a)
         const vec_t v = __builtin_bit_cast(vec_t, in[t][h]);
         if constexpr (VEC) {
           if (at < a.M) *reinterpret_cast<vec_t*>(o) = v;
+        } else if (at + V <= a.M) {
+          __builtin_memcpy(o, &v, 16);
         } else {
 #pragma unroll
           for (int i = 0; i < V; ++i)
@@ -503,7 +569,7 @@ hipError_t launch(const AdapterArgs& a, const Plan& p, hipStream_t st) {
   const auto on16 = [](const void* q) { return ((uintptr_t)q & 15) == 0; };
   const bool vec_x = a.K % V == 0 && a.ldx % V == 0 && on16(a.x) && on16(a.A);
   const bool vec_out = a.M % V == 0 && a.ldbase % V == 0 && a.ldout % V == 0 && on16(a.base) &&
-                       on16(a.out);
+                       on16(a.out) && a.R % V == 0 && on16(a.B);
 #define GDN_ADAPTER_CASE(RT)                                                   \
   if (p.rank_tiles == RT)                                                      \
     return p.rows == 64 ? launch_tiles<T, 4, RT>(a, vec_x, vec_out, st)        \

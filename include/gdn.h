@@ -568,8 +568,8 @@ typedef struct {
  *   cu_seqlens [B + 1]
  * fp32 sums; x A^T is held in fp32 and enters the second product with 16 bits (bf16) or 24 bits
  * (fp32); the sum with base is rounded once. A non-finite x, or a sum past fp32's range, reaches its
- * own row alone, where an infinite value may stand as NaN. Vectors of 16 bytes where pointers, strides
- * and sizes allow it, else element by element. Rows from cu_seqlens[B] on are not written. Every
+ * own row alone, where an infinite value may stand as NaN. Rows may start anywhere; fastest are those
+ * on 16 bytes, of whole multiples of 16 bytes. Rows from cu_seqlens[B] on are not written. Every
  * workgroup looks through the B requests: thousands of them cost some 3 us a thousand.
  * workspace: at least gdn_adapter_workspace_size bytes, 256-byte aligned. */
 size_t gdn_adapter_workspace_size(const gdn_adapter_problem_t* prob);
