@@ -28,11 +28,11 @@
 // tokens, 16 heads: 474 MB read, of 604 that the walks ask for).
 //
 // What bounds it (bf16, 128 x 128): a chunk's products and the vector work between them, 164 matrix
-// and 590 vector instructions a wave. One request of 131072 tokens, 16 heads, 712 us a call: outputs
-// 490 us at 4.4 TB/s, matrix cores busy 36 % and vector units 42 % of the time, two workgroups a CU;
-// states 215 at 2.7 (the slow heads' columns lie side by side in a row and do not reach every memory
+// and 590 vector instructions a wave. One request of 131072 tokens, 16 heads, 726 us a call: outputs
+// 490 us at 4.5 TB/s, matrix cores busy 32 % and vector units 37 % of the time, two workgroups a CU;
+// states 212 at 3.1 (the slow heads' columns lie side by side in a row and do not reach every memory
 // channel: 4.0 TB/s where all heads are slow), join 25. 8 ragged requests of 33860 tokens, 32 heads,
-// 420 us (286, 132 and 20). Gradients of 4 x 4096 tokens, 16 heads, 250 us (177, 64 and 17).
+// 425 us (279, 127 and 20). Gradients of 4 x 4096 tokens, 16 heads, 255 us (181, 65 and 17).
 //
 // Precision: bf16 inputs enter the products as they are. The decayed v of the state's update are
 // three bf16 (24 bits), since states are fp32 results. What only outputs take, which end as bf16, is

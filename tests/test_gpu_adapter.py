@@ -77,6 +77,15 @@ def test_adapter_sizes(dtype, k, m):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k,m,rank", [(1027, 333, 100), (2051, 517, 40), (4095, 263, 9), (513, 1021, 17)])
+@pytest.mark.parametrize("lengths", [[70, 1, 40], [5, 2]])
+def test_adapter_odd_rows(dtype, k, m, rank, lengths):
+    """Rows of no whole number of vectors, long enough that most of a row is read in vectors."""
+    c = make(k + rank, lengths, k, m, rank, 2, dtype, pad=5, offset=1)
+    check(c, call(c), f"adapter {dtype} K={k} M={m} R={rank}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("pad,offset", [(8, 0), (8, 8), (1, 0), (0, 3), (13, 1)])
 def test_adapter_strides_and_alignment(dtype, pad, offset):
     """Rows any stride apart, starting anywhere: vectors where all of them allow it."""
