@@ -528,18 +528,24 @@ Plan plan_of(const AdapterShape& s) {
   p.tiles = s.N / p.rows + (groups < s.N ? groups : s.N);
   p.rank_tiles = s.R <= 16 ? 1 : s.R <= 32 ? 2 : s.R <= 64 ? 4 : 8;
   const int step = s.bf16 ? 32 : 16, steps = (int)cdiv(s.K, step);
-  // Slices of K: enough workgroups for the device, at least 16 steps each. Every slice of a tile of
-  // many ranks is read again by each of its workgroups in the expansion, so these have fewer (8192
-  // rows, 4096 inputs and outputs, rank 128: 87 us with 256, 116 with 1024; 33860 rows of rank 16: 330
-  // with 1024, 334 with 512, 339 with 4096).
-  int64_t n = cdiv(p.rank_tiles <= 2 ? 1024 : 256, p.tiles);
+  // Slices of K: enough workgroups for the device, at least 16 steps each. Every slice is summed again by
+  // each of the tile's workgroups in the expansion, so where 256 workgroups are there without them there
+  // are no more than four, or two of 128 ranks (4096 inputs and outputs, 8192 rows, rank 16: 64 us with
+  // eight, 59 with four, 62 with two; rank 128: 98 with four, 88 with two).
+  int64_t n = cdiv(1024, p.tiles), most = cdiv(256, p.tiles);
+  const int64_t few = p.rank_tiles == 8 ? 2 : 4;
+  if (most < few) most = few;
+  if (n > most) n = most;
   if (n > cdiv(steps, 16)) n = cdiv(steps, 16);
   p.per_split = (int)cdiv(cdiv(steps, n), 4) * 4;
   p.splits = (int)cdiv(steps, p.per_split);
-  // Columns of a workgroup: likewise, whole turns of its four waves (33860 rows of rank 16, 8192
-  // outputs: 322 us with 4096 workgroups, 375 with 1024).
+  // Columns of a workgroup: whole turns of its four waves, four of them where 1024 workgroups are left,
+  // so that rows are asked for behind the products of a turn (rank 16, 16384 rows: 81 us with four turns,
+  // 92 with one; 33860 rows of 8192 outputs: 317 with four, 326 with eight, 368 with sixteen; rank 64:
+  // 397 with four, 466 with sixteen).
   const int unit = s.bf16 ? 256 : 128;
-  int64_t m = cdiv(p.rank_tiles <= 2 ? 4096 : 1024, p.tiles);
+  int64_t m = cdiv(1024, p.tiles);
+  if (m < cdiv(s.M, 4 * unit)) m = cdiv(s.M, 4 * unit);
   if (m > cdiv(s.M, unit)) m = cdiv(s.M, unit);
   p.cols = (int)(cdiv(cdiv(s.M, m), unit) * unit);
   p.col_blocks = (int)cdiv(s.M, p.cols);
