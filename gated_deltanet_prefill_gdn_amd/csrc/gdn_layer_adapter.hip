@@ -10,11 +10,11 @@
 // Both are bound by the bytes of x, base and out: A and B come out of the L2, and the products are
 // R / 16 instructions for every 16 rows and 32 entries. Operands go from memory to registers as the
 // matrix instructions want them (16 bytes a lane: eight bf16 or four fp32 of a row), without LDS.
-// Measured, bf16: 33860 rows of 8 prompts, 4096 inputs, 8192 outputs, rank 16: 306-318 us, the first
+// Measured, bf16: 33860 rows of 8 prompts, 4096 inputs, 8192 outputs, rank 16: 301-318 us, the first
 // launch 89 us (3.6 TB/s), the second 227 (5.2 TB/s); 512 single tokens of 32 adapters 15.4 us, each
 // launch little more than the latency of its chain: requests, rows, sums, B, base. Every workgroup of
 // the first launch looks through all requests, which is felt in the thousands: 8192 single tokens of
-// 4096 inputs and outputs take 91 us, of which some 20 are that look.
+// 4096 inputs and outputs take 83 us, of which some 23 are that look.
 //
 // Precision: fp32 sums. bf16: x A^T enters the second product as two bf16 (16 bits), since one would
 // be a rounding of its own; fp32: products of fp32 instructions. base is added in fp32, and the sum
@@ -53,7 +53,7 @@ __device__ __forceinline__ acc4 mma(u32x4 a, u32x4 b, acc4 c) {
 // they start on 16 bytes. Otherwise they start anywhere, which the memory system takes as well; where
 // they would end behind the row its last 16 bytes are read, and end_of_row() moves them into place
 // when they have arrived (8192 rows of 4095 inputs and outputs, rank 16: 128 us, 162 with every entry
-// by itself; 69 for 4096, whose rows start on 16 bytes).
+// by itself; 59 for 4096, whose rows start on 16 bytes).
 template <typename T, bool VEC>
 __device__ __forceinline__ u32x4 load_row(const T* row, int at, int n) {
   constexpr int V = kVec<T>;
